@@ -48,7 +48,9 @@ typedef enum {
   TP_ERR_UNSUPPORTED = 3,   /* valid but not implemented combination                            */
   TP_ERR_WORKSPACE = 4,     /* workspace smaller than the *_workspace() query says              */
   TP_ERR_CUDA = 5,          /* a CUDA runtime call failed (message in tp_last_error)            */
-  TP_ERR_TIMEOUT = 6        /* a bounded device-side wait ran out (tp_check_device_error)       */
+  TP_ERR_TIMEOUT = 6,       /* a bounded device-side wait ran out (tp_check_device_error)       */
+  TP_ERR_INDEX = 7          /* a device-side index (page, sequence, length) was out of range
+                               (tp_check_device_error)                                         */
 } tp_status;
 
 typedef enum { TP_F32 = 0, TP_BF16 = 1 } tp_dtype;
@@ -235,6 +237,146 @@ tp_status tp_attn_bwd(const tp_attn_desc* desc, const void* x, const void* wqkv_
  * dwk and dwv [h][n_kv*hd], dwo [n_q*hd][h]. */
 tp_status tp_attn_unpack_grads(const tp_attn_desc* desc, const void* dwqkv_p, const void* dwo_p,
                                void* dwq, void* dwk, void* dwv, void* dwo, void* stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* Rotary positions                                                                            */
+/* ------------------------------------------------------------------------------------------ */
+/* A head's first rot_dim dims are rot_dim/2 pairs; pair i of a token at position n is turned by
+ * the angle a = n * w_i and scaled by the magnitude m:
+ *   (x1, x2) -> m * (x1 cos a - x2 sin a, x1 sin a + x2 cos a);   the other dims pass through.
+ *   TP_ROPE_HALF:        pair i is dims (i, i + rot_dim/2)
+ *   TP_ROPE_INTERLEAVED: pair i is dims (2i, 2i + 1)
+ * Plain frequencies are w_i = base^(-2i/rot_dim).  For contexts longer than the original one:
+ *   TP_ROPE_LINEAR:   w_i / factor (the positions are interpolated)
+ *   TP_ROPE_NTK:      the base becomes base * factor^(rot_dim/(rot_dim-2)): the slowest pair is
+ *                     interpolated by factor, the fastest not at all
+ *   TP_ROPE_BY_PARTS: with r_i = orig_len * w_i / 2 pi (turns over the original context) and
+ *                     g = clamp((r_i - beta_slow)/(beta_fast - beta_slow), 0, 1):
+ *                     g w_i + (1 - g) w_i / factor; magnitude 1 + 0.1 ln(factor) unless given
+ * Angles are computed in 64 bits and reduced to one turn before the sine and cosine, so far
+ * positions lose nothing; the rotation is computed in fp32 and rounded once. */
+typedef enum { TP_ROPE_HALF = 0, TP_ROPE_INTERLEAVED = 1 } tp_rope_layout;
+typedef enum {
+  TP_ROPE_PLAIN = 0, TP_ROPE_LINEAR = 1, TP_ROPE_NTK = 2, TP_ROPE_BY_PARTS = 3
+} tp_rope_scaling;
+
+typedef struct {
+  int32_t rot_dim;      /* rotated dims of a head: even, >= 2                                 */
+  int32_t layout;       /* tp_rope_layout                                                     */
+  int32_t scaling;      /* tp_rope_scaling                                                    */
+  int32_t flags;        /* 0                                                                  */
+  double base;          /* > 0                                                                */
+  double factor;        /* context scale > 0 (ignored by TP_ROPE_PLAIN)                       */
+  double orig_len;      /* TP_ROPE_BY_PARTS: tokens of the original context, > 0              */
+  double beta_fast;     /* TP_ROPE_BY_PARTS: turns above which a pair is not interpolated      */
+  double beta_slow;     /* ... and below which it is interpolated fully (< beta_fast)          */
+  double magnitude;     /* m; 0 means 1 (TP_ROPE_BY_PARTS: 1 + 0.1 ln(factor))                 */
+} tp_rope_desc;
+
+/* Rows of heads: row (t, j) is head_dim consecutive elements at data + t*token_stride +
+ * j*head_stride (strides in elements, >= 0).  Describes [T][heads][head_dim] tensors, slices of
+ * them, and [heads][T][head_dim] ones.  Rows that a call writes must not overlap each other. */
+typedef struct {
+  const void* data;
+  int64_t token_stride;
+  int64_t head_stride;
+} tp_head_rows;
+
+/* The frequency table: freqs, rot_dim/2 doubles in device memory (8-byte aligned), receives
+ * w_i / 2 pi.  One-time setup, as the packing calls; the table may be used by any number of calls. */
+tp_status tp_rope_freqs(const tp_rope_desc* desc, void* freqs, void* stream);
+
+/* out = the rotation of x; inverse != 0: its gradient, m * R(-a) x (the transpose, so with
+ * x = dL/dout the result is dL/dx).  x and out: T tokens of n_heads heads of head_dim elements of
+ * dtype; out may be x with the same strides (in place), and must not overlap it otherwise.
+ * positions: int32 [T] (any sign).  Any element alignment and any head_dim in [rot_dim, 1024];
+ * 16-byte aligned rows with rot_dim/2 (half) or rot_dim (interleaved) a multiple of 16 bytes are
+ * moved in 16-byte vectors. */
+tp_status tp_rope(const tp_rope_desc* desc, int32_t dtype, int64_t T, int32_t n_heads,
+                  int32_t head_dim, const tp_head_rows* x, const void* positions,
+                  const void* freqs, int32_t inverse, const tp_head_rows* out, void* stream);
+
+/* ------------------------------------------------------------------------------------------ */
+/* Paged key/value cache                                                                       */
+/* ------------------------------------------------------------------------------------------ */
+/* The cache is a pool of n_pages pages for keys and one for values.  A page holds page_size
+ * consecutive slots of one sequence for all KV heads; element e of (page, head, slot) lies at
+ *   page*page_stride + head*head_stride + slot*slot_stride + e   (elements; all three 0: dense
+ *   [n_pages][n_kv][page_size][head_dim]; [n_pages][page_size][n_kv][head_dim] is head_stride =
+ *   head_dim, slot_stride = n_kv*head_dim).
+ * tables: int32 [b][max_pages]; slot n of sequence i is slot n % page_size of page
+ * tables[i][n / page_size].  Only the entries of slots in use are read.  Sequences may share
+ * pages that no call writes.
+ * Indices live in device memory and are checked there: an index outside its range (a page
+ * outside 0 .. n_pages-1, a sequence, a length) is never followed; the token or key is left out
+ * and tp_check_device_error() reports TP_ERR_INDEX.
+ * k_pages, v_pages: 16-byte aligned, strides multiples of 16 bytes; head_dim a multiple of 8 in
+ * [8, 256]; dtype bf16 or fp32; b <= 65535 (the library's other decode calls' limit). */
+typedef struct {
+  int64_t b;            /* sequences (rows of tables)                                         */
+  int64_t n_pages;      /* pages in the pool                                                  */
+  int64_t max_pages;    /* columns of tables                                                  */
+  int64_t page_stride, head_stride, slot_stride;
+  int32_t page_size;    /* slots per page, >= 1                                               */
+  int32_t n_q;          /* query heads                                                        */
+  int32_t n_kv;         /* KV heads; must divide n_q                                          */
+  int32_t head_dim;
+  int32_t dtype;        /* tp_dtype                                                           */
+  int32_t flags;        /* 0                                                                  */
+  float scale;          /* softmax scale; 0 means 1/sqrt(head_dim)                            */
+  int32_t reserved;
+} tp_paged_desc;
+
+/* Append T tokens' keys and values: slot slots[t] of sequence seq_ids[t] (NULL: sequence t;
+ * T <= b).  slots[t] < 0 writes nothing (padding).  k and v: rows of n_kv heads, dtype.  With
+ * rope (and its freqs), k is rotated by positions[t] (NULL: by slots[t]) before it is stored; q
+ * (rows of n_q heads, may be NULL) is rotated too, for every token, and stored in q_out (may be q
+ * with the same strides).  Without rope q must be NULL.  Two tokens of one call must not have the
+ * same slot (which of the two is kept would be undefined).  seq_ids, slots, positions: int32 [T]. */
+tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, const void* seq_ids,
+                             const void* slots, const void* tables, const tp_head_rows* k,
+                             const tp_head_rows* v, const tp_rope_desc* rope, const void* freqs,
+                             const void* positions, const tp_head_rows* q,
+                             const tp_head_rows* q_out, void* k_pages, void* v_pages,
+                             void* stream);
+
+/* Attention of one new token per sequence over its cached keys (the new token's own key among
+ * them: append it first):
+ *   o[i][j] = sum_n w_n v[n],  w = softmax_n(scale * q[i][j] . k[n]),  n = 0 .. lens[i]-1,
+ * query head j over KV head floor(j / (n_q/n_kv)).  q, o: b rows of n_q heads, dtype, 16-byte
+ * aligned with strides multiples of 16 bytes; o must not overlap q.  lens: int32 [b], between 0
+ * and max_pages*page_size; a sequence of length 0 gets o = 0.
+ *   lse: NULL or fp32 [b][n_q], receives log sum_n exp(scale q.k[n]) (-infinity for length 0).
+ *   score: NULL or fp32 [b][n_kv][max_pages*page_size]; the weights that the group's query heads
+ *   gave to each key are added: score[i][g][n] += sum_j w_n(i, j), n < lens[i]; other entries stay
+ *   as they are.
+ * The sum over the keys is split over the SMs and joined in a fixed order: equal calls on equal
+ * devices give equal results.  Slots at and past lens[i] are not read.
+ * workspace: tp_attn_decode_paged_workspace(desc, score != NULL) bytes, 16-byte aligned; its
+ * contents need not survive between calls.  It grows with b * n_q * max_pages * page_size
+ * where score is given. */
+size_t tp_attn_decode_paged_workspace(const tp_paged_desc* desc, int32_t with_score);
+tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_head_rows* q,
+                               const void* k_pages, const void* v_pages, const void* tables,
+                               const void* lens, const tp_head_rows* o, void* lse, void* score,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* Cut every sequence longer than budget back to budget keys.  Per (sequence, KV head) the last
+ * `recent` keys stay, and of the others the budget - recent with the largest score (equal scores:
+ * the lower slot; a NaN score counts as the smallest).  The kept keys, values and scores are
+ * moved to slots 0 .. budget-1 in their order, in place; the slots behind keep their old contents.
+ * Keys that were rotated keep their rotation.
+ *   score: fp32 [b][n_kv][max_pages*page_size]; lens: int32 [b]; new_lens: int32 [b] receives
+ *   min(lens, budget) (may be lens); keep: NULL or int32 [b][n_kv][budget], the kept slots in
+ *   ascending order (a sequence within the budget: 0 .. lens-1, then -1).
+ * 1 <= budget <= max_pages*page_size, 0 <= recent <= budget.  The pages of a sequence that is cut
+ * must not be shared.  Pages past slot budget-1 are free afterwards.
+ * workspace: tp_kv_evict_paged_workspace(desc, budget) bytes, 16-byte aligned. */
+size_t tp_kv_evict_paged_workspace(const tp_paged_desc* desc, int32_t budget);
+tp_status tp_kv_evict_paged(const tp_paged_desc* desc, void* score, const void* lens,
+                            int32_t budget, int32_t recent, void* k_pages, void* v_pages,
+                            const void* tables, void* new_lens, void* keep, void* workspace,
+                            size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------------------------------------ */
 /* Reduction and glue                                                                          */

@@ -25,8 +25,12 @@ What it computes, and where the method is stated:
 * ``seqpar``    -- the sequence-parallel form of the collective: reduce-scatter of the partials
                    into token slices and all-gather of the slices ("Why tensor parallelism has to
                    stay in scale-up", "Where the 320 comes from").
+* ``rope``      -- rotary positions: the pairs' angles, their scalings for longer contexts, the
+                   rotation and its gradient.
+* ``paged``     -- decode attention over a paged key/value cache with sequences of different
+                   lengths, the weights it gives to each key, and eviction by accumulated weight.
 
-Each function also has a *sharded reference mode* (loop over the p shards and add the partial
+Each function of the block also has a *sharded reference mode* (loop over the p shards and add the partial
 results in order) used only by the invariant tests that check "the sharded sum equals the
 unsharded result".
 
@@ -34,4 +38,4 @@ Everything is float64 numpy; matrix products use numpy's matmul as a library pri
 error function comes from scipy.  No blocking, fusion or reordering beyond the stated formulas.
 """
 
-from . import mlp, attention, decode, costmodel, seqpar, moe  # noqa: F401
+from . import mlp, attention, decode, costmodel, seqpar, moe, rope, paged  # noqa: F401

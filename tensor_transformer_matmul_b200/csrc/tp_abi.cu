@@ -230,6 +230,7 @@ const char* tp_status_string(int32_t s) {
     case TP_ERR_WORKSPACE: return "TP_ERR_WORKSPACE";
     case TP_ERR_CUDA: return "TP_ERR_CUDA";
     case TP_ERR_TIMEOUT: return "TP_ERR_TIMEOUT";
+    case TP_ERR_INDEX: return "TP_ERR_INDEX";
     default: return "TP_ERR_UNKNOWN";
   }
 }
@@ -247,6 +248,9 @@ tp_status tp_check_device_error(void* stream) {
   if (v) {
     const uint32_t zero = 0;
     cudaMemcpy(w, &zero, sizeof(zero), cudaMemcpyHostToDevice);
+    if (v == tp::DEVERR_INDEX)
+      return tp::set_error(TP_ERR_INDEX,
+                           "a page, sequence or length in device memory was out of range");
     return tp::set_error(TP_ERR_TIMEOUT,
                          "a bounded device wait ran out (site bits " + std::to_string(v) + ")");
   }

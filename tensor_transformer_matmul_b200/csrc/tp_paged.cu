@@ -1,0 +1,282 @@
+// Rotary positions and the paged key/value cache: argument checks and launches.
+#include "paged.cuh"
+
+using tp::set_error;
+
+namespace {
+
+tp_status check_freqs(const void* freqs) {
+  if (!freqs) return set_error(TP_ERR_INVALID_ARG, "freqs is null");
+  if (reinterpret_cast<uintptr_t>(freqs) & 7)
+    return set_error(TP_ERR_INVALID_ARG, "freqs must be 8-byte aligned");
+  return TP_OK;
+}
+
+tp_status check_ints(const void* p, const char* name) {
+  if (!p) return set_error(TP_ERR_INVALID_ARG, std::string(name) + " is null");
+  if (reinterpret_cast<uintptr_t>(p) & 3)
+    return set_error(TP_ERR_INVALID_ARG, std::string(name) + " must be 4-byte aligned");
+  return TP_OK;
+}
+
+tp_status check_vec_rows(const tp_head_rows* r, int64_t T, int heads, int hd, int eb, bool written,
+                         const char* name) {
+  tp_status st = tp::rope::check_rows(r, T, heads, hd, eb, written, name);
+  if (st != TP_OK) return st;
+  const int64_t unit = 16 / eb;
+  if ((reinterpret_cast<uintptr_t>(r->data) & 15) || r->token_stride % unit || r->head_stride % unit)
+    return set_error(TP_ERR_INVALID_ARG,
+                     std::string(name) + ": rows must be 16-byte aligned, strides multiples of 16 bytes");
+  return TP_OK;
+}
+
+tp::rope::Rows rows_of(const tp_head_rows* r) { return {r->data, r->token_stride, r->head_stride}; }
+
+size_t decode_ws(const tp::paged::View& c) {
+  return tp::align256(static_cast<size_t>(c.b * c.n_q) * 4);
+}
+
+size_t evict_ws(const tp::paged::View& c, int64_t budget) {
+  const size_t heads = static_cast<size_t>(c.b) * c.n_kv;
+  return tp::align256(heads * budget * 4) + tp::align256(heads * 4) +
+         tp::align256(static_cast<size_t>(c.b) * 4);
+}
+
+}  // namespace
+
+extern "C" tp_status tp_rope_freqs(const tp_rope_desc* desc, void* freqs, void* stream) {
+  tp::clear_error();
+  tp_status st = tp::rope::check_desc(desc);
+  if (st != TP_OK) return st;
+  if ((st = check_freqs(freqs)) != TP_OK) return st;
+  tp::rope::freqs_kernel<<<1, 128, 0, static_cast<cudaStream_t>(stream)>>>(
+      *desc, static_cast<double*>(freqs));
+  TP_LAUNCH_CHECK();
+  return TP_OK;
+}
+
+extern "C" tp_status tp_rope(const tp_rope_desc* desc, int32_t dtype, int64_t T, int32_t n_heads,
+                             int32_t head_dim, const tp_head_rows* x, const void* positions,
+                             const void* freqs, int32_t inverse, const tp_head_rows* out,
+                             void* stream) {
+  tp::clear_error();
+  tp_status st = tp::rope::check_desc(desc);
+  if (st != TP_OK) return st;
+  if (dtype != TP_F32 && dtype != TP_BF16) return set_error(TP_ERR_INVALID_ARG, "dtype");
+  if (T < 0 || n_heads < 0) return set_error(TP_ERR_SHAPE, "T and n_heads must be >= 0");
+  if (head_dim < desc->rot_dim || head_dim > 1024)
+    return set_error(TP_ERR_SHAPE, "head_dim must be in [rot_dim, 1024]");
+  if (T > INT32_MAX) return set_error(TP_ERR_SHAPE, "T must fit in 31 bits");
+  if (T == 0 || n_heads == 0) return TP_OK;
+  const int eb = tp::elem_bytes(dtype);
+  if ((st = tp::rope::check_rows(x, T, n_heads, head_dim, eb, false, "x")) != TP_OK ||
+      (st = tp::rope::check_rows(out, T, n_heads, head_dim, eb, true, "out")) != TP_OK ||
+      (st = tp::rope::check_pair(x, out, "out")) != TP_OK ||
+      (st = check_ints(positions, "positions")) != TP_OK || (st = check_freqs(freqs)) != TP_OK)
+    return st;
+  tp::rope::Args a{};
+  a.freqs = static_cast<const double*>(freqs);
+  a.positions = static_cast<const int32_t*>(positions);
+  a.T = T;
+  a.heads = n_heads;
+  a.hd = head_dim;
+  a.half = desc->rot_dim / 2;
+  a.interleaved = desc->layout == TP_ROPE_INTERLEAVED;
+  a.m = tp::rope::magnitude_of(desc);
+  a.sign = inverse ? -1.f : 1.f;
+  a.x = rows_of(x);
+  a.out = rows_of(out);
+  return tp::rope::launch(a, dtype, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, const void* seq_ids,
+                                        const void* slots, const void* tables,
+                                        const tp_head_rows* k, const tp_head_rows* v,
+                                        const tp_rope_desc* rope, const void* freqs,
+                                        const void* positions, const tp_head_rows* q,
+                                        const tp_head_rows* q_out, void* k_pages, void* v_pages,
+                                        void* stream) {
+  tp::clear_error();
+  tp::paged::AppendArgs a{};
+  tp_status st = tp::paged::check_desc(desc, &a.c);
+  if (st != TP_OK) return st;
+  if (T < 0 || T > INT32_MAX) return set_error(TP_ERR_SHAPE, "T must be >= 0 and fit in 31 bits");
+  if (!seq_ids && T > desc->b) return set_error(TP_ERR_SHAPE, "without seq_ids T must be <= b");
+  if (rope) {
+    if ((st = tp::rope::check_desc(rope)) != TP_OK) return st;
+    if (rope->rot_dim > desc->head_dim) return set_error(TP_ERR_SHAPE, "rot_dim must be <= head_dim");
+  }
+  if (!rope && q) return set_error(TP_ERR_INVALID_ARG, "q is rotated: it needs a rope desc");
+  if (!q != !q_out) return set_error(TP_ERR_INVALID_ARG, "q and q_out come together");
+  if (T == 0) return TP_OK;
+  const int eb = tp::elem_bytes(desc->dtype);
+  if (k_pages && k_pages == v_pages)
+    return set_error(TP_ERR_INVALID_ARG, "k_pages and v_pages are the same pool");
+  if ((st = tp::paged::check_pages(k_pages, v_pages, tables)) != TP_OK ||
+      (st = check_ints(slots, "slots")) != TP_OK ||
+      (st = tp::rope::check_rows(k, T, desc->n_kv, desc->head_dim, eb, false, "k")) != TP_OK ||
+      (st = tp::rope::check_rows(v, T, desc->n_kv, desc->head_dim, eb, false, "v")) != TP_OK)
+    return st;
+  if (seq_ids && (st = check_ints(seq_ids, "seq_ids")) != TP_OK) return st;
+  if (rope && (st = check_freqs(freqs)) != TP_OK) return st;
+  if (positions && (st = check_ints(positions, "positions")) != TP_OK) return st;
+  if (q && ((st = tp::rope::check_rows(q, T, desc->n_q, desc->head_dim, eb, false, "q")) != TP_OK ||
+            (st = tp::rope::check_rows(q_out, T, desc->n_q, desc->head_dim, eb, true, "q_out")) != TP_OK ||
+            (st = tp::rope::check_pair(q, q_out, "q_out")) != TP_OK))
+    return st;
+  a.c.tables = static_cast<const int32_t*>(tables);
+  a.c.err = tp::device_error_word();
+  a.seq_ids = static_cast<const int32_t*>(seq_ids);
+  a.slots = static_cast<const int32_t*>(slots);
+  a.k = rows_of(k);
+  a.v = rows_of(v);
+  a.kp = k_pages;
+  a.vp = v_pages;
+  a.rotate = rope != nullptr;
+  a.q.T = T;
+  a.q.hd = desc->head_dim;
+  a.q.sign = 1.f;
+  if (rope) {
+    a.q.freqs = static_cast<const double*>(freqs);
+    a.q.positions = static_cast<const int32_t*>(positions ? positions : slots);
+    a.q.half = rope->rot_dim / 2;
+    a.q.interleaved = rope->layout == TP_ROPE_INTERLEAVED;
+    a.q.m = tp::rope::magnitude_of(rope);
+  }
+  if (q) {
+    a.q.heads = desc->n_q;
+    a.q.x = rows_of(q);
+    a.q.out = rows_of(q_out);
+  }
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  tp::ProfScope prof(s, "kv_append");
+  const unsigned g = tp::rope::grid_for(T * (a.q.heads + 2 * desc->n_kv) * (desc->head_dim - a.q.half));
+  if (desc->dtype == TP_BF16)
+    TP_LAUNCH_PDL(tp::paged::append_kernel<__nv_bfloat16>, dim3(g), dim3(256), 0, s, a);
+  else
+    TP_LAUNCH_PDL(tp::paged::append_kernel<float>, dim3(g), dim3(256), 0, s, a);
+  return TP_OK;
+}
+
+extern "C" size_t tp_attn_decode_paged_workspace(const tp_paged_desc* desc, int32_t with_score) {
+  tp::clear_error();
+  tp::paged::View c;
+  (void)with_score;
+  return tp::paged::check_desc(desc, &c) == TP_OK ? decode_ws(c) : 0;
+}
+
+extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_head_rows* q,
+                                          const void* k_pages, const void* v_pages,
+                                          const void* tables, const void* lens,
+                                          const tp_head_rows* o, void* lse, void* score,
+                                          void* workspace, size_t ws_bytes, void* stream) {
+  tp::clear_error();
+  tp::paged::DecodeArgs a{};
+  tp_status st = tp::paged::check_desc(desc, &a.c);
+  if (st != TP_OK) return st;
+  if (desc->b == 0) return TP_OK;
+  const int eb = tp::elem_bytes(desc->dtype);
+  if ((st = tp::paged::check_pages(k_pages, v_pages, tables)) != TP_OK ||
+      (st = check_ints(lens, "lens")) != TP_OK ||
+      (st = check_vec_rows(q, desc->b, desc->n_q, desc->head_dim, eb, false, "q")) != TP_OK ||
+      (st = check_vec_rows(o, desc->b, desc->n_q, desc->head_dim, eb, true, "o")) != TP_OK)
+    return st;
+  if (lse && (st = check_ints(lse, "lse")) != TP_OK) return st;
+  if (score && (st = check_ints(score, "score")) != TP_OK) return st;
+  if (!workspace) return set_error(TP_ERR_INVALID_ARG, "workspace is null");
+  if (reinterpret_cast<uintptr_t>(workspace) & 15)
+    return set_error(TP_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  if (ws_bytes < decode_ws(a.c)) return set_error(TP_ERR_WORKSPACE, "workspace too small");
+  a.c.tables = static_cast<const int32_t*>(tables);
+  a.c.err = tp::device_error_word();
+  a.q = rows_of(q);
+  a.o = rows_of(o);
+  a.kp = k_pages;
+  a.vp = v_pages;
+  a.lens = static_cast<const int32_t*>(lens);
+  a.scale = tp::paged::scale_of(desc);
+  a.lse = static_cast<float*>(lse ? lse : workspace);
+  a.score = static_cast<float*>(score);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  {
+    tp::ProfScope prof(s, "attn_decode_paged");
+    const dim3 grid(static_cast<unsigned>(desc->n_q), static_cast<unsigned>(desc->b));
+    if (desc->dtype == TP_BF16)
+      TP_LAUNCH_PDL(tp::paged::decode_kernel<__nv_bfloat16>, grid, dim3(32), 0, s, a);
+    else
+      TP_LAUNCH_PDL(tp::paged::decode_kernel<float>, grid, dim3(32), 0, s, a);
+  }
+  if (!score) return TP_OK;
+  tp::ProfScope prof(s, "attn_score_paged");
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tp::ceil_div(a.c.cap, 4), 256)),
+                  static_cast<unsigned>(desc->n_kv), static_cast<unsigned>(desc->b));
+  if (desc->dtype == TP_BF16)
+    TP_LAUNCH_PDL(tp::paged::score_kernel<__nv_bfloat16>, grid, dim3(128), 0, s, a);
+  else
+    TP_LAUNCH_PDL(tp::paged::score_kernel<float>, grid, dim3(128), 0, s, a);
+  return TP_OK;
+}
+
+extern "C" size_t tp_kv_evict_paged_workspace(const tp_paged_desc* desc, int32_t budget) {
+  tp::clear_error();
+  tp::paged::View c;
+  if (tp::paged::check_desc(desc, &c) != TP_OK) return 0;
+  return budget >= 1 && budget <= c.cap ? evict_ws(c, budget) : 0;
+}
+
+extern "C" tp_status tp_kv_evict_paged(const tp_paged_desc* desc, void* score, const void* lens,
+                                       int32_t budget, int32_t recent, void* k_pages,
+                                       void* v_pages, const void* tables, void* new_lens,
+                                       void* keep, void* workspace, size_t ws_bytes,
+                                       void* stream) {
+  tp::clear_error();
+  tp::paged::EvictArgs a{};
+  tp_status st = tp::paged::check_desc(desc, &a.c);
+  if (st != TP_OK) return st;
+  if (budget < 1 || budget > a.c.cap)
+    return set_error(TP_ERR_SHAPE, "budget must be in [1, max_pages * page_size]");
+  if (recent < 0 || recent > budget) return set_error(TP_ERR_SHAPE, "recent must be in [0, budget]");
+  if (desc->b == 0) return TP_OK;
+  if (k_pages && k_pages == v_pages)
+    return set_error(TP_ERR_INVALID_ARG, "k_pages and v_pages are the same pool");
+  if ((st = tp::paged::check_pages(k_pages, v_pages, tables)) != TP_OK ||
+      (st = check_ints(score, "score")) != TP_OK || (st = check_ints(lens, "lens")) != TP_OK ||
+      (st = check_ints(new_lens, "new_lens")) != TP_OK)
+    return st;
+  if (keep && (st = check_ints(keep, "keep")) != TP_OK) return st;
+  if (!workspace) return set_error(TP_ERR_INVALID_ARG, "workspace is null");
+  if (reinterpret_cast<uintptr_t>(workspace) & 15)
+    return set_error(TP_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  if (ws_bytes < evict_ws(a.c, budget)) return set_error(TP_ERR_WORKSPACE, "workspace too small");
+  const size_t heads = static_cast<size_t>(a.c.b) * a.c.n_kv;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  a.c.tables = static_cast<const int32_t*>(tables);
+  a.c.err = tp::device_error_word();
+  a.score = static_cast<float*>(score);
+  a.lens = static_cast<const int32_t*>(lens);
+  a.new_lens = static_cast<int32_t*>(new_lens);
+  a.keep_out = static_cast<int32_t*>(keep);
+  a.keep = reinterpret_cast<int32_t*>(w);
+  w += tp::align256(heads * budget * 4);
+  a.cut = reinterpret_cast<int32_t*>(w);
+  w += tp::align256(heads * 4);
+  a.new_ws = reinterpret_cast<int32_t*>(w);
+  a.budget = budget;
+  a.recent = recent;
+  a.kp = k_pages;
+  a.vp = v_pages;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int eb = tp::elem_bytes(desc->dtype);
+  {
+    tp::ProfScope prof(s, "kv_evict_select");
+    TP_LAUNCH_PDL(tp::paged::evict_select_kernel,
+                  dim3(static_cast<unsigned>(desc->n_kv), static_cast<unsigned>(desc->b)),
+                  dim3(tp::paged::kEvictThreads), 0, s, a);
+  }
+  tp::ProfScope prof(s, "kv_evict_move");
+  TP_LAUNCH_PDL(tp::paged::evict_move_kernel,
+                dim3(static_cast<unsigned>(2 * desc->head_dim * eb / 16),
+                     static_cast<unsigned>(desc->n_kv), static_cast<unsigned>(desc->b)),
+                dim3(256), 0, s, a, eb);
+  return TP_OK;
+}

@@ -16,13 +16,15 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("TPBLOCK_LIBRARY") or os.path.join(_HERE, "libtpblock.so")
 
 TP_OK, TP_ERR_INVALID_ARG, TP_ERR_SHAPE, TP_ERR_UNSUPPORTED, TP_ERR_WORKSPACE, TP_ERR_CUDA, \
-    TP_ERR_TIMEOUT = range(7)
+    TP_ERR_TIMEOUT, TP_ERR_INDEX = range(8)
 TP_F32, TP_BF16 = 0, 1
 ACT = {"identity": 0, "relu": 1, "gelu": 2, "swiglu": 3}
 DTYPE = {"f32": TP_F32, "bf16": TP_BF16}
 TORCH_OF = {TP_F32: torch.float32, TP_BF16: torch.bfloat16}
 TP_REDUCE_SEPARATE, TP_REDUCE_FUSED = 0, 1
 TP_FLAG_F32_RESIDUAL = 1
+ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 
 # every symbol the header declares
 EXPORTS = (
@@ -42,7 +44,9 @@ EXPORTS = (
     "tp_moe_fwd", "tp_moe_bwd_workspace", "tp_moe_bwd", "tp_mlp_shard_sizes",
     "tp_mlp_pack_shard", "tp_mlp_fwd_shard",
     "tp_mlp_bwd_shard", "tp_attn_shard_sizes", "tp_attn_pack_shard", "tp_attn_fwd_shard",
-    "tp_attn_bwd_shard", "tp_attn_bwd_sp_workspace", "tp_attn_bwd_sp",
+    "tp_attn_bwd_shard", "tp_attn_bwd_sp_workspace", "tp_attn_bwd_sp", "tp_rope_freqs", "tp_rope",
+    "tp_kv_append_paged", "tp_attn_decode_paged_workspace", "tp_attn_decode_paged",
+    "tp_kv_evict_paged_workspace", "tp_kv_evict_paged",
 )
 
 
@@ -75,6 +79,28 @@ class tp_attn_desc(ctypes.Structure):
                 ("norm_eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
 
 
+class tp_rope_desc(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("scaling", ctypes.c_int32), ("flags", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("orig_len", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("magnitude", ctypes.c_double)]
+
+
+class tp_head_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class tp_paged_desc(ctypes.Structure):
+    _fields_ = [("b", ctypes.c_int64), ("n_pages", ctypes.c_int64), ("max_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("n_q", ctypes.c_int32), ("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
 class tp_shard_sizes(ctypes.Structure):
     _fields_ = [("col_weight_bytes", ctypes.c_size_t), ("row_weight_bytes", ctypes.c_size_t),
                 ("saved_bytes", ctypes.c_size_t), ("fwd_workspace", ctypes.c_size_t),
@@ -96,6 +122,7 @@ def load():
     P, S, I32, I64, F32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     MD, AD = ctypes.POINTER(tp_mlp_desc), ctypes.POINTER(tp_attn_desc)
     ED = ctypes.POINTER(tp_moe_desc)
+    RD, PD, HR = (ctypes.POINTER(c) for c in (tp_rope_desc, tp_paged_desc, tp_head_rows))
     sig = {
         "tp_mlp_w1_packed_bytes": (S, [MD]), "tp_mlp_w2_packed_bytes": (S, [MD]),
         "tp_mlp_pack": (I32, [MD, P, P, P, P, P, P]), "tp_mlp_saved_bytes": (S, [MD]),
@@ -144,6 +171,13 @@ def load():
         "tp_attn_bwd_shard": (I32, [AD, I32, P, P, P, P, P, P, P, P, S, P]),
         "tp_attn_bwd_sp_workspace": (S, [AD]),
         "tp_attn_bwd_sp": (I32, [AD, P, P, P, P, P, P, P, P, S, P]),
+        "tp_rope_freqs": (I32, [RD, P, P]),
+        "tp_rope": (I32, [RD, I32, I64, I32, I32, HR, P, P, I32, HR, P]),
+        "tp_kv_append_paged": (I32, [PD, I64, P, P, P, HR, HR, RD, P, P, HR, HR, P, P, P]),
+        "tp_attn_decode_paged_workspace": (S, [PD, I32]),
+        "tp_attn_decode_paged": (I32, [PD, HR, P, P, P, P, HR, P, P, P, S, P]),
+        "tp_kv_evict_paged_workspace": (S, [PD, I32]),
+        "tp_kv_evict_paged": (I32, [PD, P, P, I32, I32, P, P, P, P, P, P, S, P]),
         "tp_profile_read": (I32, [I32, ctypes.c_char_p, I32, ctypes.POINTER(ctypes.c_uint64),
                                   ctypes.POINTER(ctypes.c_double)]),
         "tp_profile_read_launch": (I32, [I32, ctypes.c_int64, ctypes.POINTER(ctypes.c_double)]),
@@ -309,6 +343,169 @@ def tp_rmsnorm(x, out, eps=1e-5, stream=None):
     rows = x.numel() // x.shape[-1] if x.numel() else 0
     _check(load().tp_rmsnorm(_ptr(x), xt, int(rows), int(x.shape[-1]), float(eps), _ptr(out), ot,
                              _stream(stream)))
+
+
+# --------------------------------------------------------------------- rotary positions
+def rope_desc(rot_dim, layout="half", base=10000.0, scaling="none", factor=1.0, orig_len=0,
+              beta_fast=32.0, beta_slow=1.0, magnitude=0.0):
+    return tp_rope_desc(int(rot_dim), ROPE_LAYOUT[layout] if isinstance(layout, str) else int(layout),
+                        ROPE_SCALING[scaling] if isinstance(scaling, str) else int(scaling), 0,
+                        float(base), float(factor), float(orig_len), float(beta_fast),
+                        float(beta_slow), float(magnitude))
+
+
+def _on(stream, *tensors):
+    """The stream to launch on.  The tensors lie on the current device, and so does the stream: a
+    launch goes to the current device, which may not be able to reach another one's memory."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev and t.numel() > 0:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    if stream.device_index != dev:
+        raise ValueError(f"stream of cuda:{stream.device_index}, but the current device is cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _want(name, t, dtype, shape=None):
+    """A contiguous tensor of the given type (and shape); its address."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(name, t, dtype, shape):
+    """A [tokens][heads][head_dim] tensor, any strides over tokens and heads."""
+    if TORCH_OF[dtype] != t.dtype:
+        raise TypeError(f"{name} must be {TORCH_OF[dtype]}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    ts, hs, es = t.stride()
+    if es != 1 and shape[2] > 1:
+        raise ValueError(f"{name}: the elements of a head must be consecutive")
+    return ctypes.byref(tp_head_rows(t.data_ptr(), ts if shape[0] > 1 else 0,
+                                     hs if shape[1] > 1 else 0))
+
+
+def tp_rope_freqs(desc, freqs, stream=None):
+    """freqs: float64 [rot_dim/2], the table that the rotations take."""
+    s = _on(stream, freqs)
+    _check(load().tp_rope_freqs(ctypes.byref(desc),
+                                _want("freqs", freqs, torch.float64, (desc.rot_dim // 2,)), s))
+
+
+def tp_rope(desc, x, positions, freqs, out, inverse=False, stream=None):
+    """out = the rotation of x ([T][heads][head_dim], strided; out may be x); ``inverse``: its
+    gradient.  positions: int32 [T]."""
+    s = _on(stream, x, positions, freqs, out)
+    T, H, hd = shape = tuple(x.shape)
+    dt = TP_BF16 if x.dtype == torch.bfloat16 else TP_F32
+    _check(load().tp_rope(ctypes.byref(desc), dt, T, H, hd, _rows("x", x, dt, shape),
+                          _want("positions", positions, torch.int32, (T,)),
+                          _want("freqs", freqs, torch.float64, (desc.rot_dim // 2,)),
+                          int(bool(inverse)), _rows("out", out, dt, shape), s))
+
+
+# ------------------------------------------------------------------ paged key/value cache
+def paged_desc(n_q, k_pages, tables, scale=0.0):
+    """The descriptor of a paged cache: k_pages [n_pages][n_kv][page_size][head_dim] (a view with
+    any strides over the first three), tables int32 [b][max_pages]."""
+    n_pages, n_kv, page, hd = k_pages.shape
+    if k_pages.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("k_pages must be bfloat16 or float32")
+    if hd > 1 and k_pages.stride(3) != 1:
+        raise ValueError("k_pages: the elements of a slot must be consecutive")
+    b, width = tables.shape
+    # a dimension of one has no stride that matters: give it one that keeps the others apart
+    st = [k_pages.stride(i) if k_pages.shape[i] > 1 else 0 for i in range(3)]
+    if not any(st):
+        st[0] = hd
+    return tp_paged_desc(int(b), n_pages, int(width), *st, page, int(n_q), n_kv, hd, _dt(k_pages),
+                         0, float(scale), 0)
+
+
+def _pages(desc, k_pages, v_pages, tables):
+    shape = (desc.n_pages, desc.n_kv, desc.page_size, desc.head_dim)
+    st = (desc.page_stride, desc.head_stride, desc.slot_stride)
+    if not any(st):   # the C declarations' dense layout
+        st = (desc.n_kv * desc.page_size * desc.head_dim, desc.page_size * desc.head_dim,
+              desc.head_dim)
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != TORCH_OF[desc.dtype] or tuple(t.shape) != shape:
+            raise ValueError(f"{name} must be {TORCH_OF[desc.dtype]} of shape {shape}")
+        for n, have, want in zip(shape, t.stride(), st + (1,)):
+            if n > 1 and have != want:
+                raise ValueError(f"{name} does not have the descriptor's strides")
+    return (k_pages.data_ptr(), v_pages.data_ptr(),
+            _want("tables", tables, torch.int32, (desc.b, desc.max_pages)))
+
+
+def tp_kv_append_paged(desc, k, v, slots, tables, k_pages, v_pages, seq_ids=None, q=None,
+                       q_out=None, rope=None, freqs=None, positions=None, stream=None):
+    """Token t's k and v ([T][n_kv][head_dim], strided) into slot slots[t] of sequence seq_ids[t]
+    (None: sequence t); with ``rope`` k is rotated by positions[t] (None: slots[t]) first, and q
+    ([T][n_q][head_dim]) into q_out."""
+    s = _on(stream, k, v, slots, tables, k_pages, v_pages, seq_ids, q, q_out, freqs, positions)
+    T = k.shape[0]
+    kv, i32 = (T, desc.n_kv, desc.head_dim), torch.int32
+    qs = (T, desc.n_q, desc.head_dim)
+    kp, vp, tb = _pages(desc, k_pages, v_pages, tables)
+    _check(load().tp_kv_append_paged(
+        ctypes.byref(desc), T, None if seq_ids is None else _want("seq_ids", seq_ids, i32, (T,)),
+        _want("slots", slots, i32, (T,)), tb, _rows("k", k, desc.dtype, kv),
+        _rows("v", v, desc.dtype, kv), None if rope is None else ctypes.byref(rope),
+        None if freqs is None else _want("freqs", freqs, torch.float64,
+                                         (rope.rot_dim // 2,) if rope is not None else None),
+        None if positions is None else _want("positions", positions, i32, (T,)),
+        None if q is None else _rows("q", q, desc.dtype, qs),
+        None if q_out is None else _rows("q_out", q_out, desc.dtype, qs), kp, vp, s))
+
+
+def tp_attn_decode_paged_workspace(desc, with_score=False):
+    return load().tp_attn_decode_paged_workspace(ctypes.byref(desc), int(bool(with_score)))
+
+
+def tp_attn_decode_paged(desc, q, k_pages, v_pages, tables, lens, o, lse=None, score=None,
+                         workspace=None, stream=None):
+    """o ([b][n_q][head_dim], strided like q) = attention of one token per sequence over its first
+    lens[i] cached keys; lse fp32 [b][n_q]; score fp32 [b][n_kv][max_pages*page_size] += the
+    weights of every key."""
+    s = _on(stream, q, k_pages, v_pages, tables, lens, o, lse, score, workspace)
+    b, f32 = desc.b, torch.float32
+    shape = (b, desc.n_q, desc.head_dim)
+    kp, vp, tb = _pages(desc, k_pages, v_pages, tables)
+    _check(load().tp_attn_decode_paged(
+        ctypes.byref(desc), _rows("q", q, desc.dtype, shape), kp, vp, tb,
+        _want("lens", lens, torch.int32, (b,)), _rows("o", o, desc.dtype, shape),
+        None if lse is None else _want("lse", lse, f32, (b, desc.n_q)),
+        None if score is None else _want("score", score, f32,
+                                         (b, desc.n_kv, desc.max_pages * desc.page_size)),
+        _ptr(workspace), _nbytes(workspace), s))
+
+
+def tp_kv_evict_paged_workspace(desc, budget):
+    return load().tp_kv_evict_paged_workspace(ctypes.byref(desc), int(budget))
+
+
+def tp_kv_evict_paged(desc, score, lens, budget, recent, k_pages, v_pages, tables, new_lens,
+                      keep=None, workspace=None, stream=None):
+    """Cut every sequence longer than ``budget`` to its ``recent`` last keys and the others with
+    the largest score; keep int32 [b][n_kv][budget] receives the kept slots."""
+    s = _on(stream, score, lens, k_pages, v_pages, tables, new_lens, keep, workspace)
+    b, i32 = desc.b, torch.int32
+    kp, vp, tb = _pages(desc, k_pages, v_pages, tables)
+    _check(load().tp_kv_evict_paged(
+        ctypes.byref(desc), _want("score", score, torch.float32,
+                                  (b, desc.n_kv, desc.max_pages * desc.page_size)),
+        _want("lens", lens, i32, (b,)), int(budget), int(recent), kp, vp, tb,
+        _want("new_lens", new_lens, i32, (b,)),
+        None if keep is None else _want("keep", keep, i32, (b, desc.n_kv, int(budget))),
+        _ptr(workspace), _nbytes(workspace), s))
 
 
 # ------------------------------------------------------------------ one shard per device
