@@ -158,101 +158,6 @@ __global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
   }
 }
 
-// ---------------------------------------------------------------------------------- decode
-struct DecodeArgs {
-  View c;
-  rope::Rows q, o;
-  const void *kp, *vp;
-  const int32_t* lens;
-  float scale;
-  float* lse;     // workspace's where the caller wants none
-  float* score;
-};
-
-// One warp per (query head, sequence): one pass over the keys with the running maximum and sum.
-template <typename T>
-__global__ void __launch_bounds__(32) decode_kernel(DecodeArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  constexpr int kMax = 8;
-  const int j = blockIdx.x, lane = threadIdx.x;
-  const int64_t seq = blockIdx.y;
-  const int g = j / a.c.group, hd = a.c.hd;
-  const T* qp = static_cast<const T*>(a.q.p) + seq * a.q.ts + j * a.q.hs;
-  T* op = static_cast<T*>(const_cast<void*>(a.o.p)) + seq * a.o.ts + j * a.o.hs;
-  const T* kp = static_cast<const T*>(a.kp);
-  const T* vp = static_cast<const T*>(a.vp);
-  float q[kMax], acc[kMax];
-#pragma unroll
-  for (int r = 0; r < kMax; ++r) {
-    const int e = lane + 32 * r;
-    q[r] = e < hd ? to_f(qp[e]) * a.scale : 0.f;
-    acc[r] = 0.f;
-  }
-  float m = -INFINITY, l = 0.f;
-  const int64_t n = a.c.keys(a.lens, seq);
-  if (lane == 0 && n != a.lens[seq]) record_device_error(a.c.err, DEVERR_INDEX);
-  bool seen = false;
-  for (int64_t i = 0; i < n; ++i) {
-    const int64_t off = a.c.at(seq, g, i);
-    if (off < 0) {
-      if (lane == 0) record_device_error(a.c.err, DEVERR_INDEX);
-      continue;
-    }
-    float dot = 0.f;
-#pragma unroll
-    for (int r = 0; r < kMax; ++r) {
-      const int e = lane + 32 * r;
-      if (e < hd) dot = fmaf(q[r], to_f(kp[off + e]), dot);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-    seen = true;
-    const float mn = fmaxf(m, dot), from = mn == -INFINITY ? 0.f : mn;
-    const float corr = expf(m - from), p = expf(dot - from);
-    l = l * corr + p;
-    m = mn;
-#pragma unroll
-    for (int r = 0; r < kMax; ++r) {
-      const int e = lane + 32 * r;
-      if (e < hd) acc[r] = acc[r] * corr + p * to_f(vp[off + e]);
-    }
-  }
-  // no key: 0; keys whose scores are all -infinity have no softmax: NaN (0 * infinity)
-  const float inv = seen ? 1.f / l : 0.f;
-#pragma unroll
-  for (int r = 0; r < kMax; ++r) {
-    const int e = lane + 32 * r;
-    if (e < hd) op[e] = from_f<T>(acc[r] * inv);
-  }
-  if (lane == 0) a.lse[seq * a.c.n_q + j] = m + logf(l);
-}
-
-// One warp per (key, KV head, sequence): the group's weights of this key, added in head order.
-template <typename T>
-__global__ void __launch_bounds__(128) score_kernel(DecodeArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const int lane = threadIdx.x & 31, g = blockIdx.y, hd = a.c.hd;
-  const int64_t seq = blockIdx.z, n = a.c.keys(a.lens, seq);
-  for (int64_t i = blockIdx.x * 4 + (threadIdx.x >> 5); i < n; i += gridDim.x * 4) {
-    const int64_t off = a.c.at(seq, g, i);
-    if (off < 0) continue;
-    const T* k = static_cast<const T*>(a.kp) + off;
-    float w = 0.f;
-    for (int h = 0; h < a.c.group; ++h) {
-      const int j = g * a.c.group + h;
-      const T* qp = static_cast<const T*>(a.q.p) + seq * a.q.ts + j * a.q.hs;
-      float dot = 0.f;
-      for (int e = lane; e < hd; e += 32) dot = fmaf(to_f(qp[e]) * a.scale, to_f(k[e]), dot);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      w += expf(dot - a.lse[seq * a.c.n_q + j]);
-    }
-    if (lane == 0) a.score[(seq * a.c.n_kv + g) * a.c.cap + i] += w;
-  }
-}
-
 // ---------------------------------------------------------------------------------- evict
 struct EvictArgs {
   View c;

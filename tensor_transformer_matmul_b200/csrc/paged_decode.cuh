@@ -1,0 +1,748 @@
+// Attention of one new token per sequence over a paged key/value cache.
+//
+// Mathematics: one pass over a sequence's keys with the running maximum m and sum l of its softmax
+// (in base 2, scores times log2 e): o = sum_n 2^(z_n - m) v_n / l.  Parts of a sequence are joined
+// by (m, l, o): each part's weight is 2^(m_part - m).  m, l, scores and o are fp32 throughout.
+//
+// What bounds it: every key and value is read once and used by the query heads of its group, a few
+// operations per byte, so the cache's bytes do.  The kernel is built around keeping loads in flight:
+//   * A warp takes 32 keys at a time and stages them itself with 16-byte asynchronous copies into
+//     its own part of shared memory, in the order in which its lanes use them.  Every lane reads
+//     back only what it copied, so there is no barrier and no bank conflict in the loop, and a
+//     page may end anywhere (a row's address is looked up per key, one table entry per lane).
+//   * bf16: scores are K q^T and the output V^T p^T with 16 x 8 x 16 matrix instructions, keys or
+//     dims as the rows and the group's heads as the 8 columns, so a group of 8 heads wastes
+//     nothing.  The order of the dims inside a product is free: a lane's 16 bytes of a row are its
+//     operands of two instructions as they lie; values are paired over two keys by byte permutes.
+//     Larger instructions (tcgen05, 64 rows or more) would need the rows staged in the layouts that
+//     their descriptors know and gain nothing on a stream that memory bounds.
+//   * fp32: products in fp32 on the SIMT units.
+//
+// Split: a unit is 32 keys of one (sequence, KV head, tile of query heads); the units of the whole
+// batch lie in one line, cut into equal runs, one per block of a grid that fills the GPU once.  So
+// one long sequence and a ragged batch load every SM alike, whatever the lengths (which only the
+// device knows).  A run that holds the whole of a (sequence, head) writes its output; the others
+// leave (m, l, o) for join_kernel.  Caches of short rows use one block per (sequence, head) and no
+// second launch.
+#pragma once
+
+#include "paged.cuh"
+#include "sm100.cuh"
+
+namespace tp {
+namespace paged {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kChunk = 32;       // keys of a unit
+
+struct DecodeArgs {
+  View c;
+  rope::Rows q, o;
+  const void *kp, *vp;
+  const int32_t* lens;
+  float scale;                   // times log2 e
+  float* lse;
+  float* score;
+  // split runs
+  int64_t* first;                // [b + 1]: units before a sequence, of one head tile
+  float* pm;                     // [2 * runs][heads of a tile]: maximum (base 2)
+  float* pl;                     // ... sum
+  float* po;                     // ... [hd]: output before the division
+  float* z;                      // [b][n_kv][cap][zw]: base-2 scores, for the weights
+  int64_t min_units;
+  int runs, tiles, zw;           // blocks; head tiles of a group; columns of z
+};
+
+// 16 bytes into shared memory; zeros where ``take`` is false (src is then not read)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+// D += A B of 16 x 8 x 16, bf16 with fp32 sums
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// maximum that scores are taken relative to: an all -infinity maximum gives weights of 0, not NaN
+__device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
+
+// ---- the two ways to multiply; lane = 4 g + t ----
+// bf16: NT tiles of 8 heads; a step is 16 keys.  A lane's scores: keys g and g + 8, heads
+// 8 nt + 2 t and the next.
+template <int HDP_, int NT>
+struct Mma {
+  using T = __nv_bfloat16;
+  static constexpr int HDP = HDP_, kHeads = 8 * NT, kStep = 16, kOwn = 2 * NT, kKeys = 2;
+  static constexpr int kCopies = HDP / 16;          // 16-byte copies of a lane, K or V of a step
+  static constexpr int kShared = 0;                 // block-wide and per-warp scratch
+  static constexpr int kWarpShared = 0;
+  uint32_t q[HDP / 32][NT][4];
+  float acc[HDP / 16][NT][4];
+
+  __device__ __forceinline__ static int head(int i, int t) { return (i >> 1) * 8 + 2 * t + (i & 1); }
+  __device__ __forceinline__ static int k_row(int c, int lane) { return (lane >> 2) + 8 * (c & 1); }
+  __device__ __forceinline__ static int k_dim(int c, int lane) { return (c >> 1) * 32 + (lane & 3) * 8; }
+  __device__ __forceinline__ static int v_row(int c, int lane) {
+    return 2 * (lane & 3) + (c & 1) + 8 * ((c >> 1) & 1);
+  }
+  __device__ __forceinline__ static int v_dim(int c, int lane) { return (c >> 2) * 64 + (lane >> 2) * 8; }
+
+  __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, float, char*, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int c = 0; c < HDP / 32; ++c)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint4 r = make_uint4(0, 0, 0, 0);
+        if (n * 8 + g < heads && c * 32 + t * 8 < hd)
+          r = *reinterpret_cast<const uint4*>(qp + (n * 8 + g) * hs + c * 32 + t * 8);
+        q[c][n][0] = r.x; q[c][n][1] = r.y; q[c][n][2] = r.z; q[c][n][3] = r.w;
+      }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < HDP / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][n][r] = 0.f;
+  }
+  __device__ __forceinline__ void scores(uint32_t kbuf, float (&z)[kOwn][kKeys], float scale, char*, int) {
+    float s[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[n][r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < HDP / 32; ++c) {
+      const uint4 x = lds16(kbuf + (2 * c) * 512), y = lds16(kbuf + (2 * c + 1) * 512);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma16816(s[n], x.x, y.x, x.y, y.y, q[c][n][0], q[c][n][1]);
+        mma16816(s[n], x.z, y.z, x.w, y.w, q[c][n][2], q[c][n][3]);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) z[2 * n + i][k] = s[n][2 * k + i] * scale;
+  }
+  __device__ __forceinline__ void rescale(const float (&corr)[kOwn]) {
+#pragma unroll
+    for (int i = 0; i < HDP / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][n][r] *= corr[2 * n + (r & 1)];
+  }
+  // The weights enter the product as two bf16 parts, value and remainder (2^-17 of a weight is
+  // left): with one part alone the output's error would grow from its own rounding's 0.0017 to
+  // about 0.0020, and the second product costs nothing on a stream that memory bounds.
+  __device__ __forceinline__ void add_values(uint32_t vbuf, const float (&p)[kOwn][kKeys], char*, int) {
+    uint32_t hi[NT][2], lo[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float a = p[2 * n][k], b = p[2 * n + 1][k];
+        const uint32_t w = pack_bf16x2(a, b);
+        hi[n][k] = transpose8x8(w);
+        lo[n][k] = transpose8x8(pack_bf16x2(a - bf16lo(w), b - bf16hi(w)));
+      }
+#pragma unroll
+    for (int v = 0; v < HDP / 64; ++v) {
+      uint32_t r[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 x = lds16(vbuf + (4 * v + k) * 512);
+        r[k][0] = x.x; r[k][1] = x.y; r[k][2] = x.z; r[k][3] = x.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = __byte_perm(r[0][i], r[1][i], 0x5410), a1 = __byte_perm(r[0][i], r[1][i], 0x7632);
+        const uint32_t a2 = __byte_perm(r[2][i], r[3][i], 0x5410), a3 = __byte_perm(r[2][i], r[3][i], 0x7632);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma16816(acc[4 * v + i][n], a0, a1, a2, a3, hi[n][0], hi[n][1]);
+          mma16816(acc[4 * v + i][n], a0, a1, a2, a3, lo[n][0], lo[n][1]);
+        }
+      }
+    }
+  }
+  // out: [kHeads][HDP] floats
+  __device__ __forceinline__ void store(float* out, int lane) const {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < HDP / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int d = (i >> 2) * 64 + g * 8 + 2 * (i & 3);
+          *reinterpret_cast<float2*>(out + (n * 8 + 2 * t + h) * HDP + d) =
+              make_float2(acc[i][n][h], acc[i][n][2 + h]);
+        }
+  }
+};
+
+// fp32: G heads (1, 4 or 8); a step is 8 keys.  Four lanes share a key's dims and then its heads:
+// a lane's scores: key g, heads HPL t and the next (G == 1: all four the same).  A lane owns four
+// dims of the output (HDP 256: eight; HDP 64: of every other key).
+template <int HDP_, int G>
+struct Simt {
+  using T = float;
+  static constexpr int HDP = HDP_, kHeads = G, kStep = 8, kOwn = G >= 4 ? G / 4 : 1, kKeys = 1;
+  static constexpr int kCopies = HDP / 16;
+  static constexpr int kShared = G * HDP * 4;
+  static constexpr int kWarpShared = 8 * G * 4;
+  static constexpr int kLanes = HDP / 4 < 32 ? HDP / 4 : 32;   // lanes of a row of V
+  static constexpr int kRows = 32 / kLanes;                    // rows of a copy of V
+  static constexpr int kCols = HDP / 4 / kLanes;               // 16-byte columns of a lane
+  float acc[G][kCols][4];
+
+  __device__ __forceinline__ static int head(int i, int t) { return G >= 4 ? t * kOwn + i : 0; }
+  __device__ __forceinline__ static int k_row(int, int lane) { return lane >> 2; }
+  __device__ __forceinline__ static int k_dim(int c, int lane) { return c * 16 + (lane & 3) * 4; }
+  __device__ __forceinline__ static int v_row(int c, int lane) {
+    return (c / kCols) * kRows + lane / kLanes;
+  }
+  __device__ __forceinline__ static int v_dim(int c, int lane) {
+    return ((c % kCols) * kLanes + lane % kLanes) * 4;
+  }
+
+  // the block's queries, scaled, in shared memory (every warp writes the same values)
+  __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, float scale,
+                                         char* sq, int lane) {
+    float* s = reinterpret_cast<float*>(sq);
+    for (int i = lane; i < G * HDP; i += 32) {
+      const int h = i / HDP, d = i % HDP;
+      s[i] = h < heads && d < hd ? qp[h * hs + d] * scale : 0.f;
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int h = 0; h < G; ++h)
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[h][c][r] = 0.f;
+  }
+  __device__ __forceinline__ void scores(uint32_t kbuf, float (&z)[kOwn][kKeys], float, char* sq, int lane) {
+    const int t = lane & 3;
+    const uint32_t qa = sm100::smem_addr(sq) + t * 16;
+    float s[G];
+#pragma unroll
+    for (int h = 0; h < G; ++h) s[h] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < kCopies; ++c) {
+      const uint4 x = lds16(kbuf + c * 512);
+#pragma unroll
+      for (int h = 0; h < G; ++h) {
+        const uint4 y = lds16(qa + (h * HDP + c * 16) * 4);
+        s[h] = fmaf(__uint_as_float(x.x), __uint_as_float(y.x), s[h]);
+        s[h] = fmaf(__uint_as_float(x.y), __uint_as_float(y.y), s[h]);
+        s[h] = fmaf(__uint_as_float(x.z), __uint_as_float(y.z), s[h]);
+        s[h] = fmaf(__uint_as_float(x.w), __uint_as_float(y.w), s[h]);
+      }
+    }
+    if constexpr (G == 1) {
+      s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+      s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
+      z[0][0] = s[0];
+    } else {
+      // halves of the heads change hands: after two exchanges a lane has the sums of its own
+      float u[G / 2];
+#pragma unroll
+      for (int h = 0; h < G / 2; ++h) {
+        const float give = t & 2 ? s[h] : s[h + G / 2], have = t & 2 ? s[h + G / 2] : s[h];
+        u[h] = have + __shfl_xor_sync(0xffffffffu, give, 2);
+      }
+#pragma unroll
+      for (int h = 0; h < G / 4; ++h) {
+        const float give = t & 1 ? u[h] : u[h + G / 4], have = t & 1 ? u[h + G / 4] : u[h];
+        z[h][0] = have + __shfl_xor_sync(0xffffffffu, give, 1);
+      }
+    }
+  }
+  __device__ __forceinline__ void rescale(const float (&corr)[kOwn]) {
+#pragma unroll
+    for (int h = 0; h < G; ++h) {
+      const float f = __shfl_sync(0xffffffffu, corr[G >= 4 ? h % kOwn : 0], G >= 4 ? h / kOwn : 0);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[h][c][r] *= f;
+    }
+  }
+  __device__ __forceinline__ void add_values(uint32_t vbuf, const float (&p)[kOwn][kKeys], char* sp, int lane) {
+    float* s = reinterpret_cast<float*>(sp);      // [G][8 keys]
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (G >= 4 || (lane & 3) == 0) s[head(i, lane & 3) * 8 + (lane >> 2)] = p[i][0];
+    __syncwarp();
+    const int sub = lane / kLanes;
+#pragma unroll
+    for (int r = 0; r < 8 / kRows; ++r) {
+      float w[G];
+#pragma unroll
+      for (int h = 0; h < G; ++h) w[h] = s[h * 8 + r * kRows + sub];
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        const uint4 x = lds16(vbuf + (r * kCols + c) * 512);
+#pragma unroll
+        for (int h = 0; h < G; ++h) {
+          acc[h][c][0] = fmaf(w[h], __uint_as_float(x.x), acc[h][c][0]);
+          acc[h][c][1] = fmaf(w[h], __uint_as_float(x.y), acc[h][c][1]);
+          acc[h][c][2] = fmaf(w[h], __uint_as_float(x.z), acc[h][c][2]);
+          acc[h][c][3] = fmaf(w[h], __uint_as_float(x.w), acc[h][c][3]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(float* out, int lane) {
+#pragma unroll
+    for (int h = 0; h < G; ++h)
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if constexpr (kRows == 2) acc[h][c][r] += __shfl_xor_sync(0xffffffffu, acc[h][c][r], 16);
+        if (lane < kLanes)
+          *reinterpret_cast<float4*>(out + h * HDP + (c * kLanes + lane) * 4) =
+              make_float4(acc[h][c][0], acc[h][c][1], acc[h][c][2], acc[h][c][3]);
+      }
+  }
+};
+
+// shared memory of a warp's ring: two steps of keys and values
+template <typename E>
+constexpr int ring_bytes() { return 4 * E::kCopies * 512; }
+template <typename E, int W>
+constexpr int decode_smem() {
+  return W * (ring_bytes<E>() + E::kWarpShared) + E::kShared + W * E::kHeads * 8;
+}
+
+// Keys k0 .. k1-1 of (sequence, KV head g), heads j0 .. j0+heads-1: this warp's share of them.
+// On return the accumulators are in the warp's ring, its maxima and sums in sm / sl.
+template <typename E, int W>
+__device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq, int g, int j0,
+                                          int heads, int k0, int k1, char* ring, char* wsh,
+                                          char* bsh, float* sm, float* sl, int warp, int lane) {
+  using T = typename E::T;
+  constexpr int NS = kChunk / E::kStep, kBuf = E::kCopies * 512;
+  const int t = lane & 3, g8 = lane >> 2, hd = a.c.hd;
+  const T* kp = static_cast<const T*>(a.kp);
+  const T* vp = static_cast<const T*>(a.vp);
+  const uint32_t buf = sm100::smem_addr(ring) + lane * 16;
+  const int32_t* table = a.c.tables + seq * a.c.max_pages;
+
+  // a lane looks up the row of one key of a chunk
+  auto page_of = [&](int key) -> int32_t {
+    return key < k1 ? table[static_cast<uint32_t>(key) / static_cast<uint32_t>(a.c.page_size)] : -1;
+  };
+  auto row_of = [&](int key, int32_t page) -> int64_t {
+    if (page < 0 || page >= a.c.n_pages) {
+      if (key < k1) record_device_error(a.c.err, DEVERR_INDEX);
+      return -1;
+    }
+    const uint32_t slot = static_cast<uint32_t>(key) % static_cast<uint32_t>(a.c.page_size);
+    return page * a.c.page_stride + g * a.c.head_stride + slot * a.c.slot_stride;
+  };
+  auto issue = [&](int64_t row, int s) {          // step s of the chunk whose rows the lanes hold
+    const uint32_t kb = buf + (s & 1) * 2 * kBuf, vb = kb + kBuf;
+#pragma unroll
+    for (int c = 0; c < E::kCopies; ++c) {        // (equal rows' exchanges are merged)
+      const int d = E::k_dim(c, lane);
+      const int64_t off = __shfl_sync(0xffffffffu, row, s * E::kStep + E::k_row(c, lane));
+      const bool take = off >= 0 && d < hd;
+      copy16(kb + c * 512, take ? kp + off + d : kp, take);
+    }
+    copy_commit();
+#pragma unroll
+    for (int c = 0; c < E::kCopies; ++c) {
+      const int d = E::v_dim(c, lane);
+      const int64_t off = __shfl_sync(0xffffffffu, row, s * E::kStep + E::v_row(c, lane));
+      const bool take = off >= 0 && d < hd;
+      copy16(vb + c * 512, take ? vp + off + d : vp, take);
+    }
+    copy_commit();
+  };
+
+  float m[E::kOwn], l[E::kOwn];
+#pragma unroll
+  for (int i = 0; i < E::kOwn; ++i) m[i] = -INFINITY, l[i] = 0.f;
+  e.clear();
+  bool seen = false;
+
+  int chunk = k0 / kChunk + warp;
+  const int end = (k1 + kChunk - 1) / kChunk;
+  int64_t row = -1;
+  uint32_t mask = 0;
+  int32_t page = -1;
+  if (chunk < end) {
+    row = row_of(chunk * kChunk + lane, page_of(chunk * kChunk + lane));
+    mask = __ballot_sync(0xffffffffu, row >= 0);
+    issue(row, 0);
+    issue(row, 1);
+    if (chunk + W < end) page = page_of((chunk + W) * kChunk + lane);
+  }
+  for (; chunk < end; chunk += W) {
+    const bool more = chunk + W < end;
+    int64_t row_n = -1;
+    uint32_t mask_n = 0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const uint32_t kb = buf + (s & 1) * 2 * kBuf;
+      const uint32_t live = (mask >> (s * E::kStep)) & ((1u << E::kStep) - 1u);
+      copy_wait<3>();                             // this step's keys are there
+      if (live) {
+        seen = true;
+        float z[E::kOwn][E::kKeys];
+        e.scores(kb, z, a.scale, bsh, lane);
+#pragma unroll
+        for (int k = 0; k < E::kKeys; ++k) {
+          const bool in = (live >> (g8 + 8 * k)) & 1u;
+          if (a.z != nullptr && in) {
+            float* zr = a.z + ((seq * a.c.n_kv + g) * a.c.cap + chunk * kChunk + s * E::kStep + g8 + 8 * k) * a.zw;
+#pragma unroll
+            for (int i = 0; i < E::kOwn; ++i) {
+              const int h = E::head(i, t);
+              if (h < heads && (E::kHeads >= 4 || t == 0)) zr[j0 - g * a.c.group + h] = z[i][k];
+            }
+          }
+          if (!in) {
+#pragma unroll
+            for (int i = 0; i < E::kOwn; ++i) z[i][k] = -INFINITY;
+          }
+        }
+        float corr[E::kOwn], base[E::kOwn];
+        bool grew = false;
+#pragma unroll
+        for (int i = 0; i < E::kOwn; ++i) {
+          float x = z[i][0];
+          if constexpr (E::kKeys == 2) x = fmaxf(x, z[i][1]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          const float mn = fmaxf(m[i], x);
+          grew |= mn > m[i];
+          base[i] = base_of(mn);
+          corr[i] = exp2f(m[i] - base[i]);
+          m[i] = mn;
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+          e.rescale(corr);
+#pragma unroll
+          for (int i = 0; i < E::kOwn; ++i) l[i] *= corr[i];
+        }
+#pragma unroll
+        for (int i = 0; i < E::kOwn; ++i)
+#pragma unroll
+          for (int k = 0; k < E::kKeys; ++k) {
+            z[i][k] = exp2f(z[i][k] - base[i]);
+            l[i] += z[i][k];
+          }
+        copy_wait<2>();                           // and its values
+        e.add_values(kb + kBuf, z, wsh, lane);
+      }
+      copy_wait<2>();                             // (nothing lands in the slot any more)
+      // the ring's slot is free: the step after the next
+      if (s + 2 < NS) {
+        issue(row, s + 2);
+      } else {
+        if (s + 2 == NS && more) {
+          const int key = (chunk + W) * kChunk + lane;
+          row_n = row_of(key, page);
+          mask_n = __ballot_sync(0xffffffffu, row_n >= 0);
+          if (chunk + 2 * W < end) page = page_of(key + W * kChunk);
+        }
+        if (more) issue(row_n, s + 2 - NS);
+        else copy_commit(), copy_commit();
+      }
+    }
+    row = row_n;
+    mask = mask_n;
+  }
+  copy_wait<0>();
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < E::kOwn; ++i) {
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+    if (g8 == 0 && (E::kHeads >= 4 || t == 0)) {
+      sm[E::head(i, t)] = m[i];
+      // a sum of 0: no key, or keys whose scores are all -infinity, which have no softmax.  The
+      // second is marked by a negative sum.
+      sl[E::head(i, t)] = seen && l[i] == 0.f ? -1.f : l[i];
+    }
+  }
+  e.store(reinterpret_cast<float*>(ring), lane);
+}
+
+// Weight of a part with maximum pm and sum pl where the joined maximum is m.
+__device__ __forceinline__ float part_weight(float pm, float pl, float m) {
+  return pl == 0.f || pl == -1.f ? 0.f : exp2f(pm - base_of(m));
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float a, float b, float c, float d) {
+  if constexpr (sizeof(T) == 2)
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+  else
+    *reinterpret_cast<float4*>(p) = make_float4(a, b, c, d);
+}
+
+// 1 / l of a joined sum; none < 0: keys without a softmax (NaN), no keys at all: 0
+__device__ __forceinline__ float inverse_sum(float l, bool none) {
+  return l == 0.f ? (none ? NAN : 0.f) : 1.f / l;
+}
+
+// Joins the warps' parts of keys k0 .. k1-1 and writes the output (slot < 0) or a part.
+template <typename E, int W>
+__device__ __forceinline__ void block_piece(const DecodeArgs& a, E& e, int64_t seq, int g, int ht,
+                                            int k0, int k1, int64_t slot, char* smem) {
+  using T = typename E::T;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  char* ring = smem + warp * ring_bytes<E>();
+  char* wsh = smem + W * ring_bytes<E>() + warp * E::kWarpShared;
+  char* bsh = smem + W * (ring_bytes<E>() + E::kWarpShared);
+  float* sm = reinterpret_cast<float*>(bsh + E::kShared);
+  float* sl = sm + W * E::kHeads;
+  const int j0 = g * a.c.group + ht * E::kHeads;
+  const int heads = min(E::kHeads, a.c.group - ht * E::kHeads);
+  const int hd = a.c.hd;
+  e.load_q(static_cast<const T*>(a.q.p) + seq * a.q.ts + j0 * a.q.hs, a.q.hs, heads, hd, a.scale, bsh, lane);
+  warp_pass<E, W>(a, e, seq, g, j0, heads, k0, k1, ring, wsh, bsh, sm + warp * E::kHeads,
+                  sl + warp * E::kHeads, warp, lane);
+  __syncthreads();
+  const int cols = hd / 4;
+  for (int i = tid; i < heads * cols; i += W * 32) {
+    const int h = i / cols, d = (i - h * cols) * 4;
+    float mx = -INFINITY;
+    bool none = false;
+#pragma unroll
+    for (int w = 0; w < W; ++w) mx = fmaxf(mx, sm[w * E::kHeads + h]);
+    float l = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float pl = sl[w * E::kHeads + h], f = part_weight(sm[w * E::kHeads + h], pl, mx);
+      none |= pl == -1.f;
+      if (pl == 0.f || pl == -1.f) continue;
+      const float4 x = *reinterpret_cast<const float4*>(smem + w * ring_bytes<E>() + (h * E::HDP + d) * 4);
+      l = fmaf(pl, f, l);
+      s.x = fmaf(x.x, f, s.x); s.y = fmaf(x.y, f, s.y);
+      s.z = fmaf(x.z, f, s.z); s.w = fmaf(x.w, f, s.w);
+    }
+    if (slot < 0) {
+      const float inv = inverse_sum(l, none);
+      T* o = static_cast<T*>(const_cast<void*>(a.o.p)) + seq * a.o.ts + (j0 + h) * a.o.hs + d;
+      store4(o, s.x * inv, s.y * inv, s.z * inv, s.w * inv);
+      if (d == 0) a.lse[seq * a.c.n_q + j0 + h] = fmaf(mx, kLn2, logf(l));
+    } else {
+      *reinterpret_cast<float4*>(a.po + (slot * E::kHeads + h) * hd + d) = s;
+      if (d == 0) {
+        a.pm[slot * E::kHeads + h] = mx;
+        a.pl[slot * E::kHeads + h] = l == 0.f && none ? -1.f : l;
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// One block per (head tile, KV head, sequence).
+template <typename E, int W>
+__global__ void __launch_bounds__(W * 32) decode_whole_kernel(const __grid_constant__ DecodeArgs a) {
+  extern __shared__ __align__(128) char smem[];
+  pdl_wait();
+  pdl_trigger();
+  const int64_t seq = blockIdx.y;
+  const int n = static_cast<int>(a.c.keys(a.lens, seq));
+  if (blockIdx.x == 0 && threadIdx.x == 0 && n != a.lens[seq]) record_device_error(a.c.err, DEVERR_INDEX);
+  E e;
+  block_piece<E, W>(a, e, seq, blockIdx.x / a.tiles, blockIdx.x % a.tiles, 0, n, -1, smem);
+}
+
+// units per run: at least min_units, so that short work is not cut into parts that cost more to
+// join than to compute
+__device__ __forceinline__ int64_t units_per_run(const DecodeArgs& a, int64_t units) {
+  const int64_t even = (units + a.runs - 1) / a.runs;
+  return even > a.min_units ? even : a.min_units;
+}
+
+// One block per run of units.
+template <typename E, int W>
+__global__ void __launch_bounds__(W * 32) decode_split_kernel(const __grid_constant__ DecodeArgs a) {
+  extern __shared__ __align__(128) char smem[];
+  __shared__ int64_t s_sum[W], s_seq, s_first;
+  pdl_wait();
+  pdl_trigger();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t tiles = static_cast<int64_t>(a.c.n_kv) * a.tiles;
+  auto chunks = [&](int64_t seq) { return (a.c.keys(a.lens, seq) + kChunk - 1) / kChunk; };
+  // units before this thread's sequences
+  const int64_t per_thread = (a.c.b + W * 32 - 1) / (W * 32);
+  const int64_t q0 = min(tid * per_thread, a.c.b), q1 = min(q0 + per_thread, a.c.b);
+  int64_t sum = 0;
+  for (int64_t s = q0; s < q1; ++s) sum += chunks(s);
+  int64_t x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_sum[warp] = x;
+  __syncthreads();
+  int64_t before = x - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  const int64_t units = total * tiles, per = units_per_run(a, units);
+  const int64_t u0 = blockIdx.x * per, u1 = min(u0 + per, units);
+  if (blockIdx.x == 0) {
+    int64_t at = before;
+    for (int64_t s = q0; s < q1; ++s) {
+      a.first[s] = at;
+      at += chunks(s);
+      if (a.c.keys(a.lens, s) != a.lens[s]) record_device_error(a.c.err, DEVERR_INDEX);
+    }
+    if (tid == 0) a.first[a.c.b] = total;
+  }
+  if (u0 >= units) return;
+  if (sum > 0 && before * tiles <= u0 && u0 < (before + sum) * tiles) {
+    int64_t s = q0, at = before;
+    while ((at + chunks(s)) * tiles <= u0) at += chunks(s++);
+    s_seq = s;
+    s_first = at;
+  }
+  __syncthreads();
+  int64_t seq = s_seq, first = s_first * tiles, u = u0;
+  E e;
+  while (u < u1) {
+    const int64_t n = chunks(seq);
+    if (n == 0 || u >= first + n * tiles) {
+      first += n * tiles;
+      ++seq;
+      continue;
+    }
+    const int64_t tile = (u - first) / n, begin = first + tile * n;
+    const int64_t stop = min(begin + n, u1);
+    const int k0 = static_cast<int>(u - begin) * kChunk;
+    const int k1 = static_cast<int>(min((stop - begin) * kChunk, a.c.keys(a.lens, seq)));
+    const bool whole = u == begin && stop == begin + n;
+    block_piece<E, W>(a, e, seq, static_cast<int>(tile / a.tiles), static_cast<int>(tile % a.tiles), k0,
+                      k1, whole ? -1 : 2 * static_cast<int64_t>(blockIdx.x) + (u == u0 ? 0 : 1), smem);
+    u = stop;
+  }
+}
+
+// One block per (query head, sequence) that was cut: its parts, in the order of its keys.
+template <typename T, int kHeads>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeArgs a) {
+  __shared__ float4 s_o[4][64];
+  __shared__ float s_l[4];
+  __shared__ int s_none[4];
+  pdl_wait();
+  pdl_trigger();
+  const int j = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.hd;
+  const int64_t seq = blockIdx.y, tiles = static_cast<int64_t>(a.c.n_kv) * a.tiles;
+  const int64_t f = a.first[seq], n = a.first[seq + 1] - f, per = units_per_run(a, a.first[a.c.b] * tiles);
+  const int g = j / a.c.group, ht = (j - g * a.c.group) / kHeads, h = (j - g * a.c.group) % kHeads;
+  const int64_t u0 = f * tiles + (static_cast<int64_t>(g) * a.tiles + ht) * n, u1 = u0 + n;
+  T* o = static_cast<T*>(const_cast<void*>(a.o.p)) + seq * a.o.ts + j * a.o.hs;
+  if (n == 0) {
+    for (int d = tid * 4; d < hd; d += 512) store4(o + d, 0.f, 0.f, 0.f, 0.f);
+    if (tid == 0) a.lse[seq * a.c.n_q + j] = -INFINITY;
+    return;
+  }
+  const int64_t c0 = u0 / per, c1 = (u1 - 1) / per;
+  if (c0 == c1) return;
+  auto slot = [&](int64_t c) { return (2 * c + (c == c0 && u0 > c0 * per ? 1 : 0)) * kHeads + h; };
+  float mx = -INFINITY;
+  for (int64_t c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, a.pm[slot(c)]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+  float l = 0.f;
+  bool none = false;
+  float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+  for (int64_t c = c0 + warp; c <= c1; c += 4) {
+    const int64_t at = slot(c);
+    const float pl = a.pl[at], w = part_weight(a.pm[at], pl, mx);
+    const bool has = !(pl == 0.f || pl == -1.f);
+    none |= pl == -1.f;
+    if (has) l = fmaf(pl, w, l);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int d = (r * 32 + lane) * 4;
+      if (d >= hd || !has) continue;
+      const float4 x = *reinterpret_cast<const float4*>(a.po + at * hd + d);
+      s[r].x = fmaf(x.x, w, s[r].x); s[r].y = fmaf(x.y, w, s[r].y);
+      s[r].z = fmaf(x.z, w, s[r].z); s[r].w = fmaf(x.w, w, s[r].w);
+    }
+  }
+  s_o[warp][lane] = s[0];
+  s_o[warp][32 + lane] = s[1];
+  if (lane == 0) s_l[warp] = l, s_none[warp] = none;
+  __syncthreads();
+  l = s_l[0] + s_l[1] + s_l[2] + s_l[3];
+  const float inv = inverse_sum(l, s_none[0] | s_none[1] | s_none[2] | s_none[3]);
+  if (tid * 4 < hd) {
+    float4 x = s_o[0][tid];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) {
+      x.x += s_o[w][tid].x; x.y += s_o[w][tid].y;
+      x.z += s_o[w][tid].z; x.w += s_o[w][tid].w;
+    }
+    store4(o + tid * 4, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+  }
+  if (tid == 0) a.lse[seq * a.c.n_q + j] = fmaf(mx, kLn2, logf(l));
+}
+
+// score += the group's weights of each key, heads in order.
+static __global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ DecodeArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.y;
+  const int64_t seq = blockIdx.z, sg = seq * a.c.n_kv + g;
+  const int n = static_cast<int>(a.c.keys(a.lens, seq));
+  const float* lse = a.lse + seq * a.c.n_q + g * a.c.group;
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
+    if (a.c.at(seq, g, i) < 0) continue;
+    const float* z = a.z + (sg * a.c.cap + i) * a.zw;
+    float w = 0.f;
+    for (int h = 0; h < a.c.group; ++h) w += exp2f(z[h] - lse[h] * kLog2e);
+    a.score[sg * a.c.cap + i] += w;
+  }
+}
+
+}  // namespace paged
+}  // namespace tp

@@ -1,5 +1,6 @@
 // Rotary positions and the paged key/value cache: argument checks and launches.
 #include "paged.cuh"
+#include "paged_decode.cuh"
 
 using tp::set_error;
 
@@ -32,8 +33,65 @@ tp_status check_vec_rows(const tp_head_rows* r, int64_t T, int heads, int hd, in
 
 tp::rope::Rows rows_of(const tp_head_rows* r) { return {r->data, r->token_stride, r->head_stride}; }
 
-size_t decode_ws(const tp::paged::View& c) {
-  return tp::align256(static_cast<size_t>(c.b * c.n_q) * 4);
+// ---- decode attention: which kernel, and its workspace ----
+// Caches whose rows hold at most this many keys: one block per (sequence, KV head, head tile).
+constexpr int64_t kWholeKeys = 512;
+
+// heads of a tile and blocks of a split launch per SM: of the padded head size and the group
+struct DecodePlan {
+  int hdp, heads, tiles, warps, runs;
+  bool whole;
+};
+
+DecodePlan decode_plan(const tp::paged::View& c, int dtype) {
+  DecodePlan p;
+  p.hdp = c.hd <= 64 ? 64 : c.hd <= 128 ? 128 : 256;
+  if (dtype == TP_BF16) p.heads = c.group > 8 && p.hdp < 256 ? 16 : 8;
+  else p.heads = c.group == 1 ? 1 : c.group <= 4 ? 4 : 8;
+  p.tiles = static_cast<int>(tp::ceil_div(c.group, p.heads));
+  p.whole = c.cap <= kWholeKeys;
+  p.runs = tp::num_sms() * (p.hdp == 64 ? 5 : p.hdp == 128 ? 3 : 1);
+  return p;
+}
+
+struct DecodeWs {
+  size_t lse, first, pm, pl, po, z, total;
+};
+DecodeWs decode_ws(const tp::paged::View& c, int dtype, bool with_score) {
+  const DecodePlan p = decode_plan(c, dtype);
+  DecodeWs w{};
+  size_t at = 0;
+  auto take = [&](size_t bytes) { const size_t x = at; at += tp::align256(bytes); return x; };
+  const size_t parts = p.whole ? 0 : static_cast<size_t>(2) * p.runs * p.heads;
+  w.lse = take(static_cast<size_t>(c.b) * c.n_q * 4);
+  w.first = take(p.whole ? 0 : static_cast<size_t>(c.b + 1) * 8);
+  w.pm = take(parts * 4);
+  w.pl = take(parts * 4);
+  w.po = take(parts * c.hd * 4);
+  w.z = take(with_score ? static_cast<size_t>(c.b) * c.n_q * c.cap * 4 : 0);
+  w.total = at;
+  return w;
+}
+
+template <typename E>
+tp_status launch_decode(const tp::paged::DecodeArgs& a, const DecodePlan& p, cudaStream_t s) {
+  using namespace tp::paged;
+  constexpr int kWhole = E::HDP == 256 ? 4 : 8, kSplit = E::HDP == 256 ? 6 : 4;
+  const int smem = p.whole ? decode_smem<E, kWhole>() : decode_smem<E, kSplit>();
+  auto* whole = decode_whole_kernel<E, kWhole>;
+  auto* split = decode_split_kernel<E, kSplit>;
+  auto* kern = p.whole ? whole : split;
+  TP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  tp::ProfScope prof(s, "attn_decode_paged");
+  if (p.whole) {
+    TP_LAUNCH_PDL(whole, dim3(static_cast<unsigned>(a.c.n_kv * a.tiles), static_cast<unsigned>(a.c.b)),
+                  dim3(kWhole * 32), smem, s, a);
+    return TP_OK;
+  }
+  TP_LAUNCH_PDL(split, dim3(static_cast<unsigned>(a.runs)), dim3(kSplit * 32), smem, s, a);
+  auto* join = join_kernel<typename E::T, E::kHeads>;
+  TP_LAUNCH_PDL(join, dim3(static_cast<unsigned>(a.c.n_q), static_cast<unsigned>(a.c.b)), dim3(128), 0, s, a);
+  return TP_OK;
 }
 
 size_t evict_ws(const tp::paged::View& c, int64_t budget) {
@@ -161,8 +219,7 @@ extern "C" tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, co
 extern "C" size_t tp_attn_decode_paged_workspace(const tp_paged_desc* desc, int32_t with_score) {
   tp::clear_error();
   tp::paged::View c;
-  (void)with_score;
-  return tp::paged::check_desc(desc, &c) == TP_OK ? decode_ws(c) : 0;
+  return tp::paged::check_desc(desc, &c) == TP_OK ? decode_ws(c, desc->dtype, with_score != 0).total : 0;
 }
 
 extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_head_rows* q,
@@ -186,7 +243,8 @@ extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_he
   if (!workspace) return set_error(TP_ERR_INVALID_ARG, "workspace is null");
   if (reinterpret_cast<uintptr_t>(workspace) & 15)
     return set_error(TP_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
-  if (ws_bytes < decode_ws(a.c)) return set_error(TP_ERR_WORKSPACE, "workspace too small");
+  const DecodeWs w = decode_ws(a.c, desc->dtype, score != nullptr);
+  if (ws_bytes < w.total) return set_error(TP_ERR_WORKSPACE, "workspace too small");
   a.c.tables = static_cast<const int32_t*>(tables);
   a.c.err = tp::device_error_word();
   a.q = rows_of(q);
@@ -194,26 +252,37 @@ extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_he
   a.kp = k_pages;
   a.vp = v_pages;
   a.lens = static_cast<const int32_t*>(lens);
-  a.scale = tp::paged::scale_of(desc);
-  a.lse = static_cast<float*>(lse ? lse : workspace);
+  a.scale = tp::paged::scale_of(desc) * tp::paged::kLog2e;
+  const DecodePlan p = decode_plan(a.c, desc->dtype);
+  char* ws = static_cast<char*>(workspace);
+  a.lse = static_cast<float*>(lse ? lse : ws + w.lse);
   a.score = static_cast<float*>(score);
+  a.first = reinterpret_cast<int64_t*>(ws + w.first);
+  a.pm = reinterpret_cast<float*>(ws + w.pm);
+  a.pl = reinterpret_cast<float*>(ws + w.pl);
+  a.po = reinterpret_cast<float*>(ws + w.po);
+  a.z = score ? reinterpret_cast<float*>(ws + w.z) : nullptr;
+  a.zw = a.c.group;
+  a.tiles = p.tiles;
+  a.runs = p.runs;
+  a.min_units = 4;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  {
-    tp::ProfScope prof(s, "attn_decode_paged");
-    const dim3 grid(static_cast<unsigned>(desc->n_q), static_cast<unsigned>(desc->b));
-    if (desc->dtype == TP_BF16)
-      TP_LAUNCH_PDL(tp::paged::decode_kernel<__nv_bfloat16>, grid, dim3(32), 0, s, a);
-    else
-      TP_LAUNCH_PDL(tp::paged::decode_kernel<float>, grid, dim3(32), 0, s, a);
-  }
-  if (!score) return TP_OK;
+  using tp::paged::Mma;
+  using tp::paged::Simt;
+#define TP_DECODE(H)                                                                             \
+  (desc->dtype == TP_BF16                                                                        \
+       ? (p.heads == 8 ? launch_decode<Mma<H, 1>>(a, p, s)                                       \
+                       : launch_decode<Mma<H, H == 256 ? 1 : 2>>(a, p, s))                       \
+       : (p.heads == 1 ? launch_decode<Simt<H, 1>>(a, p, s)                                      \
+                       : p.heads == 4 ? launch_decode<Simt<H, 4>>(a, p, s)                       \
+                                      : launch_decode<Simt<H, 8>>(a, p, s)))
+  st = p.hdp == 64 ? TP_DECODE(64) : p.hdp == 128 ? TP_DECODE(128) : TP_DECODE(256);
+#undef TP_DECODE
+  if (st != TP_OK || !score) return st;
   tp::ProfScope prof(s, "attn_score_paged");
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tp::ceil_div(a.c.cap, 4), 256)),
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tp::ceil_div(a.c.cap, 256), 256)),
                   static_cast<unsigned>(desc->n_kv), static_cast<unsigned>(desc->b));
-  if (desc->dtype == TP_BF16)
-    TP_LAUNCH_PDL(tp::paged::score_kernel<__nv_bfloat16>, grid, dim3(128), 0, s, a);
-  else
-    TP_LAUNCH_PDL(tp::paged::score_kernel<float>, grid, dim3(128), 0, s, a);
+  TP_LAUNCH_PDL(tp::paged::weights_kernel, grid, dim3(256), 0, s, a);
   return TP_OK;
 }
 
