@@ -92,71 +92,24 @@ inline tp_status check_pages(const void* k, const void* v, const void* tables) {
 }
 
 // ---------------------------------------------------------------------------------- append
-struct AppendArgs {
-  View c;
-  rope::Args q;              // q rows (heads == 0: none); its freqs, positions and layout serve k
+// The cache as the destination of a token's k and v rows (rope.cuh moves them).
+struct Target {
   rope::Rows k, v;
+  void *kp, *vp;
+  int64_t head_stride;
+  int n_kv;
+  View c;
   const int32_t* seq_ids;
   const int32_t* slots;
-  void *kp, *vp;
-  int rotate;
-};
-
-// One thread per pair (or dim that passes through) of every q, k and v row of every token.
-template <typename T>
-__global__ void __launch_bounds__(256) append_kernel(AppendArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const int half = a.rotate ? a.q.half : 0;
-  const int per = a.c.hd - half;
-  const int rows = a.q.heads + 2 * a.c.n_kv;
-  const int64_t n = a.q.T * rows * per;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int e = static_cast<int>(i % per);
-    const int64_t row = i / per;
-    const int64_t t = row / rows;
-    int j = static_cast<int>(row - t * rows);
-    const T* x;
-    T* o;
-    bool turn = half > 0;
-    if (j < a.q.heads) {
-      x = static_cast<const T*>(a.q.x.p) + t * a.q.x.ts + j * a.q.x.hs;
-      o = static_cast<T*>(const_cast<void*>(a.q.out.p)) + t * a.q.out.ts + j * a.q.out.hs;
-    } else {
-      j -= a.q.heads;
-      const bool is_v = j >= a.c.n_kv;
-      const int g = is_v ? j - a.c.n_kv : j;
-      const int64_t slot = a.slots[t];
-      if (slot < 0) continue;
-      const int64_t seq = a.seq_ids ? a.seq_ids[t] : t;
-      const int64_t off = seq >= 0 && seq < a.c.b && slot < a.c.cap ? a.c.at(seq, g, slot) : -1;
-      if (off < 0) {
-        if (e == 0) record_device_error(a.c.err, DEVERR_INDEX);
-        continue;
-      }
-      const rope::Rows& src = is_v ? a.v : a.k;
-      x = static_cast<const T*>(src.p) + t * src.ts + g * src.hs;
-      o = static_cast<T*>(is_v ? a.vp : a.kp) + off;
-      if (is_v) turn = false;
-    }
-    if (!turn) {   // a v row moves as it is: both dims of a pair
-      if (e < half) o[e] = x[e];
-      o[e + half] = x[e + half];
-      continue;
-    }
-    if (e >= half) {
-      o[e + half] = x[e + half];
-      continue;
-    }
-    float c, s;
-    rope::cos_sin(a.q.positions[t], a.q.freqs[e], a.q.m, c, s);
-    const int e1 = a.q.interleaved ? 2 * e : e, e2 = a.q.interleaved ? 2 * e + 1 : e + half;
-    const float x1 = to_f(x[e1]), x2 = to_f(x[e2]);
-    o[e1] = from_f<T>(x1 * c - x2 * s);
-    o[e2] = from_f<T>(x1 * s + x2 * c);
+  __device__ __forceinline__ int64_t slot(int64_t t, bool report) const {
+    const int64_t n = slots[t];
+    if (n < 0) return -1;
+    const int64_t seq = seq_ids ? seq_ids[t] : t;
+    const int64_t off = seq >= 0 && seq < c.b && n < c.cap ? c.at(seq, 0, n) : -1;
+    if (off < 0 && report) record_device_error(c.err, DEVERR_INDEX);
+    return off;
   }
-}
+};
 
 // ---------------------------------------------------------------------------------- evict
 struct EvictArgs {

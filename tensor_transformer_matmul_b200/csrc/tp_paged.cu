@@ -121,7 +121,8 @@ extern "C" tp_status tp_rope(const tp_rope_desc* desc, int32_t dtype, int64_t T,
   tp_status st = tp::rope::check_desc(desc);
   if (st != TP_OK) return st;
   if (dtype != TP_F32 && dtype != TP_BF16) return set_error(TP_ERR_INVALID_ARG, "dtype");
-  if (T < 0 || n_heads < 0) return set_error(TP_ERR_SHAPE, "T and n_heads must be >= 0");
+  if (T < 0 || n_heads < 0 || n_heads > 65535)
+    return set_error(TP_ERR_SHAPE, "T must be >= 0 and n_heads in [0, 65535]");
   if (head_dim < desc->rot_dim || head_dim > 1024)
     return set_error(TP_ERR_SHAPE, "head_dim must be in [rot_dim, 1024]");
   if (T > INT32_MAX) return set_error(TP_ERR_SHAPE, "T must fit in 31 bits");
@@ -144,7 +145,11 @@ extern "C" tp_status tp_rope(const tp_rope_desc* desc, int32_t dtype, int64_t T,
   a.sign = inverse ? -1.f : 1.f;
   a.x = rows_of(x);
   a.out = rows_of(out);
-  return tp::rope::launch(a, dtype, static_cast<cudaStream_t>(stream));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  tp::ProfScope prof(s, "rope");
+  const tp::rope::NoCache none{};
+  return dtype == TP_BF16 ? tp::rope::launch_rows<__nv_bfloat16>(a, none, true, s)
+                          : tp::rope::launch_rows<float>(a, none, true, s);
 }
 
 extern "C" tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, const void* seq_ids,
@@ -155,8 +160,9 @@ extern "C" tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, co
                                         const tp_head_rows* q_out, void* k_pages, void* v_pages,
                                         void* stream) {
   tp::clear_error();
-  tp::paged::AppendArgs a{};
-  tp_status st = tp::paged::check_desc(desc, &a.c);
+  tp::paged::Target c{};
+  tp::rope::Args a{};
+  tp_status st = tp::paged::check_desc(desc, &c.c);
   if (st != TP_OK) return st;
   if (T < 0 || T > INT32_MAX) return set_error(TP_ERR_SHAPE, "T must be >= 0 and fit in 31 bits");
   if (!seq_ids && T > desc->b) return set_error(TP_ERR_SHAPE, "without seq_ids T must be <= b");
@@ -182,38 +188,36 @@ extern "C" tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, co
             (st = tp::rope::check_rows(q_out, T, desc->n_q, desc->head_dim, eb, true, "q_out")) != TP_OK ||
             (st = tp::rope::check_pair(q, q_out, "q_out")) != TP_OK))
     return st;
-  a.c.tables = static_cast<const int32_t*>(tables);
-  a.c.err = tp::device_error_word();
-  a.seq_ids = static_cast<const int32_t*>(seq_ids);
-  a.slots = static_cast<const int32_t*>(slots);
-  a.k = rows_of(k);
-  a.v = rows_of(v);
-  a.kp = k_pages;
-  a.vp = v_pages;
-  a.rotate = rope != nullptr;
-  a.q.T = T;
-  a.q.hd = desc->head_dim;
-  a.q.sign = 1.f;
+  c.c.tables = static_cast<const int32_t*>(tables);
+  c.c.err = tp::device_error_word();
+  c.seq_ids = static_cast<const int32_t*>(seq_ids);
+  c.slots = static_cast<const int32_t*>(slots);
+  c.k = rows_of(k);
+  c.v = rows_of(v);
+  c.kp = k_pages;
+  c.vp = v_pages;
+  c.head_stride = c.c.head_stride;
+  c.n_kv = desc->n_kv;
+  a.T = T;
+  a.hd = desc->head_dim;
+  a.sign = 1.f;
   if (rope) {
-    a.q.freqs = static_cast<const double*>(freqs);
-    a.q.positions = static_cast<const int32_t*>(positions ? positions : slots);
-    a.q.half = rope->rot_dim / 2;
-    a.q.interleaved = rope->layout == TP_ROPE_INTERLEAVED;
-    a.q.m = tp::rope::magnitude_of(rope);
+    a.freqs = static_cast<const double*>(freqs);
+    a.positions = static_cast<const int32_t*>(positions ? positions : slots);
+    a.half = rope->rot_dim / 2;
+    a.interleaved = rope->layout == TP_ROPE_INTERLEAVED;
+    a.m = tp::rope::magnitude_of(rope);
   }
   if (q) {
-    a.q.heads = desc->n_q;
-    a.q.x = rows_of(q);
-    a.q.out = rows_of(q_out);
+    a.heads = desc->n_q;
+    a.x = rows_of(q);
+    a.out = rows_of(q_out);
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   tp::ProfScope prof(s, "kv_append");
-  const unsigned g = tp::rope::grid_for(T * (a.q.heads + 2 * desc->n_kv) * (desc->head_dim - a.q.half));
-  if (desc->dtype == TP_BF16)
-    TP_LAUNCH_PDL(tp::paged::append_kernel<__nv_bfloat16>, dim3(g), dim3(256), 0, s, a);
-  else
-    TP_LAUNCH_PDL(tp::paged::append_kernel<float>, dim3(g), dim3(256), 0, s, a);
-  return TP_OK;
+  const bool vec = tp::rope::vector_rows(c.k, 16 / eb) && tp::rope::vector_rows(c.v, 16 / eb);
+  return desc->dtype == TP_BF16 ? tp::rope::launch_rows<__nv_bfloat16>(a, c, vec, s)
+                                : tp::rope::launch_rows<float>(a, c, vec, s);
 }
 
 extern "C" size_t tp_attn_decode_paged_workspace(const tp_paged_desc* desc, int32_t with_score) {

@@ -165,7 +165,7 @@ def test_rope_arguments(lib):
     A, S = lib.TP_ERR_INVALID_ARG, lib.TP_ERR_SHAPE
     assert _rope(lib, None) == A
     assert _rope(lib, d, dtype=2) == A
-    for bad in (dict(T=-1), dict(heads=-1), dict(hd=1032), dict(hd=63), dict(T=1 << 31)):
+    for bad in (dict(T=-1), dict(heads=-1), dict(heads=65536), dict(hd=1032), dict(hd=63), dict(T=1 << 31)):
         assert _rope(lib, d, **bad) == S
     assert _rope(lib, d, positions=None) == A and _rope(lib, d, positions=ODD) == A
     assert _rope(lib, d, freqs=None) == A and _rope(lib, d, freqs=ctypes.c_void_p(0x1004)) == A
