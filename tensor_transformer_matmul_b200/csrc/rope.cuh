@@ -7,9 +7,28 @@
 #include <algorithm>
 #include <cmath>
 
+#include "sm100.cuh"
 #include "tp_common.cuh"
 
 namespace tp {
+
+// 16 bytes into shared memory; zeros where ``take`` is false (src is then not read)
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
 namespace rope {
 
 struct Rows {
@@ -64,87 +83,117 @@ struct NoCache {
   __device__ __forceinline__ int64_t slot(int64_t, bool) const { return -1; }
 };
 
+// A warp's share: a slice of a token's rows, ``step`` of them at once.
+struct Share {
+  int slices, rows, step, items;
+};
+constexpr int kRotateWarps = 4, kRotateSteps = 24, kRotateRing = 8;
+
 // 16-byte vectors: an item is one vector of a row (interleaved pairs, or dims that pass through) or
-// two, half a rotation apart.  A thread takes the same item of kRows rows of a token: their loads
-// are issued together, and the sines and cosines (about 40 instructions a pair, in 64 bits up to
-// the reduced angle) are shared by the rows, computed while the loads fly.  Bound by the bytes
-// moved, each once.
-template <typename T, int kVecs, int kRows, typename Cache>
-__global__ void __launch_bounds__(256) rotate_rows_kernel(const __grid_constant__ Args a,
-                                                          const __grid_constant__ Cache c,
-                                                          int pass_items) {
-  constexpr int VE = 16 / sizeof(T), kPairs = VE * kVecs / 2;
+// two, half a rotation apart.  A warp has a slice of a token's rows, a lane the same item of every
+// step-th row.  The vectors are copied asynchronously into a ring of shared memory, eight of a lane
+// in flight, each lane reading back what it copied itself; while the first ones fly the warp
+// computes the token's sines and cosines (64-bit products up to the reduced angle), each once, for
+// all rows of the slice.  No warp waits for another.  Bound by the bytes moved.
+template <typename T, int kVecs, typename Cache>
+__global__ void __launch_bounds__(kRotateWarps * 32) rotate_rows_kernel(
+    const __grid_constant__ Args a, const __grid_constant__ Cache c, const __grid_constant__ Share sh) {
+  constexpr int VE = 16 / sizeof(T), kPairs = VE * kVecs / 2, kDepth = kRotateRing / kVecs;
+  constexpr int kWide = kPairs < 4 ? 2 : 4;
+  extern __shared__ __align__(16) char smem[];           // [warp][ring][32] vectors, [warp][2][half]
   pdl_wait();
   pdl_trigger();
-  const int turn_items = a.half * 2 / (VE * kVecs), items = turn_items + pass_items;
-  const int rows = a.heads + 2 * c.n_kv, groups = (rows + kRows - 1) / kRows;
-  const uint32_t per = static_cast<uint32_t>(groups) * items;
-  const int64_t n = a.T * per;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * 256) {
-    const int64_t t = n <= UINT32_MAX ? static_cast<uint32_t>(i) / per : i / per;
-    const uint32_t in = static_cast<uint32_t>(i - t * per);
-    const int r = in / static_cast<uint32_t>(items), e = in - r * items;
-    const bool turn = e < turn_items;
-    const int d = turn ? e * VE : 2 * a.half + (e - turn_items) * VE;
-    const int vecs = turn ? kVecs : 1;
-    const int32_t pos = turn ? a.positions[t] : 0;
-    const int64_t slot = c.n_kv > 0 ? c.slot(t, in == 0) : -1;
-    uint4 x[kRows][kVecs];
-    T* to[kRows];
-    bool is_v[kRows];
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      int j = r + k * groups;
-      to[k] = nullptr;
-      is_v[k] = false;
-      if (j >= rows) continue;
-      const T* from;
-      if (j < a.heads) {
-        from = static_cast<const T*>(a.x.p) + t * a.x.ts + j * a.x.hs + d;
-        to[k] = static_cast<T*>(const_cast<void*>(a.out.p)) + t * a.out.ts + j * a.out.hs + d;
-      } else {
-        if (slot < 0) continue;
-        j -= a.heads;
-        is_v[k] = j >= c.n_kv;
-        j -= is_v[k] ? c.n_kv : 0;
-        const Rows& src = is_v[k] ? c.v : c.k;
-        from = static_cast<const T*>(src.p) + t * src.ts + j * src.hs + d;
-        to[k] = static_cast<T*>(is_v[k] ? c.vp : c.kp) + slot + j * c.head_stride + d;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, turn_items = a.half * 2 / (VE * kVecs);
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * kRotateWarps + warp;
+  const int64_t t = w / sh.slices;
+  if (t >= a.T) return;
+  const int slice = static_cast<int>(w - t * sh.slices);
+  const uint32_t ring = sm100::smem_addr(smem) + warp * kRotateRing * 512 + lane * 16;
+  float* s_cos = reinterpret_cast<float*>(smem + kRotateWarps * kRotateRing * 512) + warp * 2 * a.half;
+  float* s_sin = s_cos + a.half;
+  const int all = a.heads + 2 * c.n_kv, r_begin = slice * sh.rows, r_end = min(all, r_begin + sh.rows);
+  const int steps = (r_end - r_begin + sh.step - 1) / sh.step;
+  int64_t slot = -1;
+  for (int e0 = 0; e0 < sh.items; e0 += 32) {            // (rows of more than 32 items)
+    const int q = sh.items > 32 ? 0 : lane / sh.items;
+    const int e = sh.items > 32 ? e0 + lane : lane - q * sh.items;
+    const bool pair = e < turn_items;
+    const int d = pair ? e * VE : 2 * a.half + (e - turn_items) * VE;
+    const int r0 = r_begin + q, r1 = q < sh.step && e < sh.items ? r_end : 0;
+    const T* xq = static_cast<const T*>(a.x.p) + t * a.x.ts + d;
+    const T* xk = static_cast<const T*>(c.k.p) + t * c.k.ts + d;
+    const T* xv = static_cast<const T*>(c.v.p) + t * c.v.ts + d;
+    auto issue = [&](int s) {
+      const int row = r0 + s * sh.step, j = row - a.heads;
+      const T* from = j < 0 ? xq + row * a.x.hs : j < c.n_kv ? xk + j * c.k.hs : xv + (j - c.n_kv) * c.v.hs;
+      const uint32_t to = ring + (s % kDepth) * (kVecs * 512);
+      if (row < r1) {
+        copy16(to, from, true);
+        if (kVecs == 2 && pair) copy16(to + 512, from + a.half, true);
       }
+      copy_commit();
+    };
 #pragma unroll
-      for (int v = 0; v < kVecs; ++v)
-        if (v < vecs) x[k][v] = *reinterpret_cast<const uint4*>(from + v * a.half);
+    for (int s = 0; s < kDepth; ++s) issue(s);
+    if (e0 == 0) {
+      if (a.half > 0) {
+        const int32_t pos = a.positions[t];
+        for (int i = lane; i < a.half; i += 32) {
+          float y, z;
+          cos_sin(pos, a.freqs[i], a.m, y, z);
+          s_cos[i] = y;
+          s_sin[i] = z * a.sign;
+        }
+      }
+      if (c.n_kv > 0) slot = c.slot(t, lane == 0 && slice == 0);
+      __syncwarp();
     }
     float co[kPairs], si[kPairs];
-    if (turn) {
+    if (pair) {
 #pragma unroll
-      for (int q = 0; q < kPairs; ++q) {
-        cos_sin(pos, a.freqs[e * kPairs + q], a.m, co[q], si[q]);
-        si[q] *= a.sign;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      if (!to[k]) continue;
-      if (turn && !is_v[k]) {
-        T y[VE * kVecs];
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) *reinterpret_cast<uint4*>(y + v * VE) = x[k][v];
-#pragma unroll
-        for (int q = 0; q < kPairs; ++q) {
-          const int e1 = kVecs == 2 ? q : 2 * q, e2 = kVecs == 2 ? VE + q : 2 * q + 1;
-          const float x1 = to_f(y[e1]), x2 = to_f(y[e2]);
-          y[e1] = from_f<T>(x1 * co[q] - x2 * si[q]);
-          y[e2] = from_f<T>(x1 * si[q] + x2 * co[q]);
+      for (int i = 0; i < kPairs; i += kWide) {
+        if constexpr (kWide == 2) {
+          *reinterpret_cast<float2*>(co + i) = *reinterpret_cast<const float2*>(s_cos + e * kPairs + i);
+          *reinterpret_cast<float2*>(si + i) = *reinterpret_cast<const float2*>(s_sin + e * kPairs + i);
+        } else {
+          *reinterpret_cast<float4*>(co + i) = *reinterpret_cast<const float4*>(s_cos + e * kPairs + i);
+          *reinterpret_cast<float4*>(si + i) = *reinterpret_cast<const float4*>(s_sin + e * kPairs + i);
         }
-#pragma unroll
-        for (int v = 0; v < kVecs; ++v) x[k][v] = *reinterpret_cast<const uint4*>(y + v * VE);
       }
-#pragma unroll
-      for (int v = 0; v < kVecs; ++v)
-        if (v < vecs) *reinterpret_cast<uint4*>(to[k] + v * a.half) = x[k][v];
     }
+    T* oq = static_cast<T*>(const_cast<void*>(a.out.p)) + t * a.out.ts + d;
+    T* ok = static_cast<T*>(c.kp) + slot + d;
+    T* ov = static_cast<T*>(c.vp) + slot + d;
+    for (int s = 0; s < steps; ++s) {
+      const int row = r0 + s * sh.step, j = row - a.heads;
+      copy_wait<kDepth - 1>();
+      if (row < r1 && (j < 0 || slot >= 0)) {
+        const uint32_t at = ring + (s % kDepth) * (kVecs * 512);
+        uint4 x[kVecs];
+        x[0] = lds16(at);
+        if (kVecs == 2 && pair) x[kVecs - 1] = lds16(at + 512);
+        T* to = j < 0 ? oq + row * a.out.hs : j < c.n_kv ? ok + j * c.head_stride
+                                                         : ov + (j - c.n_kv) * c.head_stride;
+        if (pair && j < c.n_kv) {
+          T y[VE * kVecs];
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v) *reinterpret_cast<uint4*>(y + v * VE) = x[v];
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) {
+            const int e1 = kVecs == 2 ? i : 2 * i, e2 = kVecs == 2 ? VE + i : 2 * i + 1;
+            const float x1 = to_f(y[e1]), x2 = to_f(y[e2]);
+            y[e1] = from_f<T>(x1 * co[i] - x2 * si[i]);
+            y[e2] = from_f<T>(x1 * si[i] + x2 * co[i]);
+          }
+#pragma unroll
+          for (int v = 0; v < kVecs; ++v) x[v] = *reinterpret_cast<const uint4*>(y + v * VE);
+        }
+        *reinterpret_cast<uint4*>(to) = x[0];
+        if (kVecs == 2 && pair) *reinterpret_cast<uint4*>(to + a.half) = x[kVecs - 1];
+      }
+      issue(s + kDepth);
+    }
+    copy_wait<0>();
   }
 }
 
@@ -270,19 +319,25 @@ inline tp_status launch_rows(const Args& a, const Cache& c, bool vectors, cudaSt
     // in place the dims that pass through stay where they are
     const int pass = c.n_kv == 0 && a.x.p == a.out.p ? 0 : (a.hd - rot) / VE;
     const int64_t items = rot / (VE * vecs) + pass;
-    // four rows to a thread once that fills the GPU; one row each is faster for a few tokens
-    // (64 tokens of 80 rows of 128 bf16 dims: see the figures at the entry point)
-    const bool many = a.T * ceil_div(rows, 4) * items >= static_cast<int64_t>(num_sms()) * 512;
-    const int64_t n = a.T * ceil_div(rows, many ? 4 : 1) * items;
-    const unsigned g = static_cast<unsigned>(std::min<int64_t>(ceil_div(n, 256), 1 << 24));
-#define TP_ROTATE(V, R) \
-  TP_LAUNCH_PDL((rotate_rows_kernel<T, V, R, Cache>), dim3(g), dim3(256), 0, s, a, c, pass)
-    if (a.interleaved) {
-      if (many) TP_ROTATE(1, 4); else TP_ROTATE(1, 1);
-    } else {
-      if (many) TP_ROTATE(2, 4); else TP_ROTATE(2, 1);
-    }
-#undef TP_ROTATE
+    // Slices of at most 24 steps of a warp's rows (the angles' cost is then small), and of fewer
+    // where the GPU would have less than 8 warps an SM (24 are no faster: 2051 tokens of 16 fp32 rows
+    // of 96 dims 7.7 and 8.1 us, 6300 tokens of 40 bf16 rows of 128 dims 26.5 and 27.6 us).
+    Share sh;
+    sh.items = static_cast<int>(items);
+    sh.step = items >= 32 ? 1 : static_cast<int>(32 / items);
+    const int64_t steps = ceil_div(rows, sh.step);
+    const int64_t slices = std::max(ceil_div(steps, kRotateSteps),
+                                    std::min(steps, ceil_div(num_sms() * 8, a.T)));
+    sh.rows = static_cast<int>(ceil_div(steps, slices)) * sh.step;
+    sh.slices = static_cast<int>(ceil_div(rows, sh.rows));
+    const int64_t blocks = ceil_div(a.T * sh.slices, kRotateWarps);
+    if (blocks > INT32_MAX) return set_error(TP_ERR_SHAPE, "too many rows");
+    const dim3 g(static_cast<unsigned>(blocks)), threads(kRotateWarps * 32);
+    const size_t smem = static_cast<size_t>(kRotateWarps) * (kRotateRing * 512 + a.half * 8);
+    if (a.interleaved)
+      TP_LAUNCH_PDL((rotate_rows_kernel<T, 1, Cache>), g, threads, smem, s, a, c, sh);
+    else
+      TP_LAUNCH_PDL((rotate_rows_kernel<T, 2, Cache>), g, threads, smem, s, a, c, sh);
     return TP_OK;
   }
   const int64_t n = a.T * rows * (a.hd - a.half);
