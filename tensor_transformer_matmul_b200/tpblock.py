@@ -8,6 +8,7 @@ error behaviour are documented in ``include/tp_block.h``.
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -122,7 +123,8 @@ def load():
     P, S, I32, I64, F32 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     MD, AD = ctypes.POINTER(tp_mlp_desc), ctypes.POINTER(tp_attn_desc)
     ED = ctypes.POINTER(tp_moe_desc)
-    RD, PD, HR = (ctypes.POINTER(c) for c in (tp_rope_desc, tp_paged_desc, tp_head_rows))
+    RD, PD = ctypes.POINTER(tp_rope_desc), ctypes.POINTER(tp_paged_desc)
+    HR = P   # tp_head_rows by address: the wrappers pass them packed
     sig = {
         "tp_mlp_w1_packed_bytes": (S, [MD]), "tp_mlp_w2_packed_bytes": (S, [MD]),
         "tp_mlp_pack": (I32, [MD, P, P, P, P, P, P]), "tp_mlp_saved_bytes": (S, [MD]),
@@ -354,61 +356,80 @@ def rope_desc(rot_dim, layout="half", base=10000.0, scaling="none", factor=1.0, 
                         float(beta_slow), float(magnitude))
 
 
-def _on(stream, *tensors):
-    """The stream to launch on.  The tensors lie on the current device, and so does the stream: a
-    launch goes to the current device, which may not be able to reach another one's memory."""
+def _device_and_stream(stream):
+    """The current device and the stream to launch on.  Tensors and stream lie on the current
+    device: a launch goes there, and it may not be able to reach another one's memory."""
     dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev and t.numel() > 0:
-            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{dev}")
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
     if stream.device_index != dev:
         raise ValueError(f"stream of cuda:{stream.device_index}, but the current device is cuda:{dev}")
-    return stream.cuda_stream
+    return dev, stream.cuda_stream
 
 
-def _want(name, t, dtype, shape=None):
-    """A contiguous tensor of the given type (and shape); its address."""
-    if t.dtype != dtype:
+def _elsewhere(name, t, dev):
+    return ValueError(f"{name} is on {t.device}, but the current device is cuda:{dev}")
+
+
+def _want(name, t, dev, dtype, shape):
+    """The address of a contiguous tensor of the given type and shape on the device."""
+    if t.get_device() != dev:
+        raise _elsewhere(name, t, dev)
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _rows(name, t, dtype, shape):
-    """A [tokens][heads][head_dim] tensor, any strides over tokens and heads."""
-    if TORCH_OF[dtype] != t.dtype:
-        raise TypeError(f"{name} must be {TORCH_OF[dtype]}")
-    if tuple(t.shape) != shape:
+_pack_rows = struct.Struct("@Pqq").pack
+
+
+def _rows(name, t, dev, dtype, shape):
+    """The tp_head_rows of a [tokens][heads][head_dim] tensor, any strides over tokens and heads."""
+    if t.get_device() != dev:
+        raise _elsewhere(name, t, dev)
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
     ts, hs, es = t.stride()
     if es != 1 and shape[2] > 1:
         raise ValueError(f"{name}: the elements of a head must be consecutive")
-    return ctypes.byref(tp_head_rows(t.data_ptr(), ts if shape[0] > 1 else 0,
-                                     hs if shape[1] > 1 else 0))
+    return _pack_rows(t.data_ptr(), ts if shape[0] > 1 else 0, hs if shape[1] > 1 else 0)
+
+
+def _scratch(t, dev):
+    """Address and bytes of a workspace."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev:
+        raise _elsewhere("workspace", t, dev)
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def tp_rope_freqs(desc, freqs, stream=None):
     """freqs: float64 [rot_dim/2], the table that the rotations take."""
-    s = _on(stream, freqs)
+    dev, s = _device_and_stream(stream)
     _check(load().tp_rope_freqs(ctypes.byref(desc),
-                                _want("freqs", freqs, torch.float64, (desc.rot_dim // 2,)), s))
+                                _want("freqs", freqs, dev, torch.float64, (desc.rot_dim // 2,)), s))
 
 
 def tp_rope(desc, x, positions, freqs, out, inverse=False, stream=None):
     """out = the rotation of x ([T][heads][head_dim], strided; out may be x); ``inverse``: its
     gradient.  positions: int32 [T]."""
-    s = _on(stream, x, positions, freqs, out)
-    T, H, hd = shape = tuple(x.shape)
-    dt = TP_BF16 if x.dtype == torch.bfloat16 else TP_F32
-    _check(load().tp_rope(ctypes.byref(desc), dt, T, H, hd, _rows("x", x, dt, shape),
-                          _want("positions", positions, torch.int32, (T,)),
-                          _want("freqs", freqs, torch.float64, (desc.rot_dim // 2,)),
-                          int(bool(inverse)), _rows("out", out, dt, shape), s))
+    dev, s = _device_and_stream(stream)
+    T, H, hd = shape = x.shape
+    dt = torch.bfloat16 if x.dtype is torch.bfloat16 else torch.float32
+    _check(load().tp_rope(ctypes.byref(desc), TP_BF16 if dt is torch.bfloat16 else TP_F32, T, H, hd,
+                          _rows("x", x, dev, dt, shape),
+                          _want("positions", positions, dev, torch.int32, (T,)),
+                          _want("freqs", freqs, dev, torch.float64, (desc.rot_dim // 2,)),
+                          1 if inverse else 0, _rows("out", out, dev, dt, shape), s))
 
 
 # ------------------------------------------------------------------ paged key/value cache
@@ -429,20 +450,26 @@ def paged_desc(n_q, k_pages, tables, scale=0.0):
                          0, float(scale), 0)
 
 
-def _pages(desc, k_pages, v_pages, tables):
-    shape = (desc.n_pages, desc.n_kv, desc.page_size, desc.head_dim)
-    st = (desc.page_stride, desc.head_stride, desc.slot_stride)
-    if not any(st):   # the C declarations' dense layout
-        st = (desc.n_kv * desc.page_size * desc.head_dim, desc.page_size * desc.head_dim,
-              desc.head_dim)
+def _pages(desc, dev, k_pages, v_pages, tables):
+    """(addresses of k_pages, v_pages and tables), (b, n_q, n_kv, head_dim, slots of a table row),
+    the element type."""
+    b, n_pages, width, ps, hs, ss = (desc.b, desc.n_pages, desc.max_pages, desc.page_stride,
+                                     desc.head_stride, desc.slot_stride)
+    page, n_kv, hd, dt = desc.page_size, desc.n_kv, desc.head_dim, TORCH_OF.get(desc.dtype)
+    if not (ps or hs or ss):   # the C declarations' dense layout
+        ss, hs, ps = hd, page * hd, n_kv * page * hd
+    shape, want = (n_pages, n_kv, page, hd), (ps, hs, ss, 1)
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype != TORCH_OF[desc.dtype] or tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be {TORCH_OF[desc.dtype]} of shape {shape}")
-        for n, have, want in zip(shape, t.stride(), st + (1,)):
-            if n > 1 and have != want:
-                raise ValueError(f"{name} does not have the descriptor's strides")
-    return (k_pages.data_ptr(), v_pages.data_ptr(),
-            _want("tables", tables, torch.int32, (desc.b, desc.max_pages)))
+        if t.get_device() != dev:
+            raise _elsewhere(name, t, dev)
+        if t.dtype is not dt or t.shape != shape:
+            raise ValueError(f"{name} must be {dt} of shape {shape}")
+        st = t.stride()
+        if st != want and any(n > 1 and x != y for n, x, y in zip(shape, st, want)):
+            raise ValueError(f"{name} does not have the descriptor's strides")
+    return ((k_pages.data_ptr(), v_pages.data_ptr(),
+             _want("tables", tables, dev, torch.int32, (b, width))),
+            (b, desc.n_q, n_kv, hd, width * page), dt)
 
 
 def tp_kv_append_paged(desc, k, v, slots, tables, k_pages, v_pages, seq_ids=None, q=None,
@@ -450,20 +477,21 @@ def tp_kv_append_paged(desc, k, v, slots, tables, k_pages, v_pages, seq_ids=None
     """Token t's k and v ([T][n_kv][head_dim], strided) into slot slots[t] of sequence seq_ids[t]
     (None: sequence t); with ``rope`` k is rotated by positions[t] (None: slots[t]) first, and q
     ([T][n_q][head_dim]) into q_out."""
-    s = _on(stream, k, v, slots, tables, k_pages, v_pages, seq_ids, q, q_out, freqs, positions)
+    dev, s = _device_and_stream(stream)
+    (kp, vp, tb), (_, n_q, n_kv, hd, _), dt = _pages(desc, dev, k_pages, v_pages, tables)
     T = k.shape[0]
-    kv, i32 = (T, desc.n_kv, desc.head_dim), torch.int32
-    qs = (T, desc.n_q, desc.head_dim)
-    kp, vp, tb = _pages(desc, k_pages, v_pages, tables)
+    per_token, i32, rows = (T,), torch.int32, (T, n_kv, hd)
+    if freqs is not None:
+        freqs = _want("freqs", freqs, dev, torch.float64,
+                      freqs.shape if rope is None else (rope.rot_dim // 2,))
     _check(load().tp_kv_append_paged(
-        ctypes.byref(desc), T, None if seq_ids is None else _want("seq_ids", seq_ids, i32, (T,)),
-        _want("slots", slots, i32, (T,)), tb, _rows("k", k, desc.dtype, kv),
-        _rows("v", v, desc.dtype, kv), None if rope is None else ctypes.byref(rope),
-        None if freqs is None else _want("freqs", freqs, torch.float64,
-                                         (rope.rot_dim // 2,) if rope is not None else None),
-        None if positions is None else _want("positions", positions, i32, (T,)),
-        None if q is None else _rows("q", q, desc.dtype, qs),
-        None if q_out is None else _rows("q_out", q_out, desc.dtype, qs), kp, vp, s))
+        ctypes.byref(desc), T,
+        None if seq_ids is None else _want("seq_ids", seq_ids, dev, i32, per_token),
+        _want("slots", slots, dev, i32, per_token), tb, _rows("k", k, dev, dt, rows),
+        _rows("v", v, dev, dt, rows), None if rope is None else ctypes.byref(rope), freqs,
+        None if positions is None else _want("positions", positions, dev, i32, per_token),
+        None if q is None else _rows("q", q, dev, dt, (T, n_q, hd)),
+        None if q_out is None else _rows("q_out", q_out, dev, dt, (T, n_q, hd)), kp, vp, s))
 
 
 def tp_attn_decode_paged_workspace(desc, with_score=False):
@@ -475,17 +503,16 @@ def tp_attn_decode_paged(desc, q, k_pages, v_pages, tables, lens, o, lse=None, s
     """o ([b][n_q][head_dim], strided like q) = attention of one token per sequence over its first
     lens[i] cached keys; lse fp32 [b][n_q]; score fp32 [b][n_kv][max_pages*page_size] += the
     weights of every key."""
-    s = _on(stream, q, k_pages, v_pages, tables, lens, o, lse, score, workspace)
-    b, f32 = desc.b, torch.float32
-    shape = (b, desc.n_q, desc.head_dim)
-    kp, vp, tb = _pages(desc, k_pages, v_pages, tables)
+    dev, s = _device_and_stream(stream)
+    (kp, vp, tb), (b, n_q, n_kv, hd, cap), dt = _pages(desc, dev, k_pages, v_pages, tables)
+    rows = (b, n_q, hd)
+    ws, n = _scratch(workspace, dev)
     _check(load().tp_attn_decode_paged(
-        ctypes.byref(desc), _rows("q", q, desc.dtype, shape), kp, vp, tb,
-        _want("lens", lens, torch.int32, (b,)), _rows("o", o, desc.dtype, shape),
-        None if lse is None else _want("lse", lse, f32, (b, desc.n_q)),
-        None if score is None else _want("score", score, f32,
-                                         (b, desc.n_kv, desc.max_pages * desc.page_size)),
-        _ptr(workspace), _nbytes(workspace), s))
+        ctypes.byref(desc), _rows("q", q, dev, dt, rows), kp, vp, tb,
+        _want("lens", lens, dev, torch.int32, (b,)), _rows("o", o, dev, dt, rows),
+        None if lse is None else _want("lse", lse, dev, torch.float32, (b, n_q)),
+        None if score is None else _want("score", score, dev, torch.float32, (b, n_kv, cap)),
+        ws, n, s))
 
 
 def tp_kv_evict_paged_workspace(desc, budget):
@@ -496,16 +523,15 @@ def tp_kv_evict_paged(desc, score, lens, budget, recent, k_pages, v_pages, table
                       keep=None, workspace=None, stream=None):
     """Cut every sequence longer than ``budget`` to its ``recent`` last keys and the others with
     the largest score; keep int32 [b][n_kv][budget] receives the kept slots."""
-    s = _on(stream, score, lens, k_pages, v_pages, tables, new_lens, keep, workspace)
-    b, i32 = desc.b, torch.int32
-    kp, vp, tb = _pages(desc, k_pages, v_pages, tables)
+    dev, s = _device_and_stream(stream)
+    (kp, vp, tb), (b, _, n_kv, _, cap), _ = _pages(desc, dev, k_pages, v_pages, tables)
+    i32, budget = torch.int32, int(budget)
+    ws, n = _scratch(workspace, dev)
     _check(load().tp_kv_evict_paged(
-        ctypes.byref(desc), _want("score", score, torch.float32,
-                                  (b, desc.n_kv, desc.max_pages * desc.page_size)),
-        _want("lens", lens, i32, (b,)), int(budget), int(recent), kp, vp, tb,
-        _want("new_lens", new_lens, i32, (b,)),
-        None if keep is None else _want("keep", keep, i32, (b, desc.n_kv, int(budget))),
-        _ptr(workspace), _nbytes(workspace), s))
+        ctypes.byref(desc), _want("score", score, dev, torch.float32, (b, n_kv, cap)),
+        _want("lens", lens, dev, i32, (b,)), budget, int(recent), kp, vp, tb,
+        _want("new_lens", new_lens, dev, i32, (b,)),
+        None if keep is None else _want("keep", keep, dev, i32, (b, n_kv, budget)), ws, n, s))
 
 
 # ------------------------------------------------------------------ one shard per device

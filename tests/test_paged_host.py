@@ -191,10 +191,12 @@ def test_python_checks(lib):
     with pytest.raises(ValueError):
         lib.paged_desc(8, kp.transpose(2, 3), tables)
     with pytest.raises(ValueError):
-        lib._pages(d, kp, slot_major, tables)       # the pools' strides differ
+        lib._pages(d, -1, kp, slot_major, tables)       # the pools' strides differ
     with pytest.raises(TypeError):
-        lib._pages(d, kp, kp, tables.long())
+        lib._pages(d, -1, kp, kp, tables.long())
     with pytest.raises(ValueError):
-        lib._pages(d, kp, kp, tables[:1])
+        lib._pages(d, -1, kp, kp, tables[:1])
     with pytest.raises(ValueError):
-        lib._rows("q", torch.zeros(2, 64, 8).transpose(1, 2), lib.TP_F32, (2, 8, 64))
+        lib._rows("q", torch.zeros(2, 64, 8).transpose(1, 2), -1, torch.float32, (2, 8, 64))
+    with pytest.raises(ValueError):
+        lib._rows("q", torch.zeros(2, 8, 64), 0, torch.float32, (2, 8, 64))     # not on the device
