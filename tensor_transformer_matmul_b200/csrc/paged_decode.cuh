@@ -68,6 +68,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+constexpr float kSlack = 8.f;
+// 2^x by the hardware's instruction (relative error 2^-22; results below 2^-126 are zeros)
+__device__ __forceinline__ float exp2_f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // maximum that scores are taken relative to: an all -infinity maximum gives weights of 0, not NaN
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
 
@@ -85,12 +92,16 @@ struct Mma {
   float acc[HDP / 16][NT][4];
 
   __device__ __forceinline__ static int head(int i, int t) { return (i >> 1) * 8 + 2 * t + (i & 1); }
-  __device__ __forceinline__ static int k_row(int c, int lane) { return (lane >> 2) + 8 * (c & 1); }
-  __device__ __forceinline__ static int k_dim(int c, int lane) { return (c >> 1) * 32 + (lane & 3) * 8; }
-  __device__ __forceinline__ static int v_row(int c, int lane) {
-    return 2 * (lane & 3) + (c & 1) + 8 * ((c >> 1) & 1);
+  // a lane copies kKRows rows of keys and kVRows of values of a step; copy c is of row c % k?Rows
+  static constexpr int kKRows = 2, kVRows = 4;
+  __device__ __forceinline__ static int k_row(int i, int lane) { return (lane >> 2) + 8 * i; }
+  __device__ __forceinline__ static int k_lane(int lane) { return (lane & 3) * 8; }
+  __device__ __forceinline__ static constexpr int k_dim(int c) { return (c >> 1) * 32; }
+  __device__ __forceinline__ static int v_row(int i, int lane) {
+    return 2 * (lane & 3) + (i & 1) + 8 * (i >> 1);
   }
-  __device__ __forceinline__ static int v_dim(int c, int lane) { return (c >> 2) * 64 + (lane >> 2) * 8; }
+  __device__ __forceinline__ static int v_lane(int lane) { return (lane >> 2) * 8; }
+  __device__ __forceinline__ static constexpr int v_dim(int c) { return (c >> 2) * 64; }
 
   __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, float, char*, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -113,18 +124,18 @@ struct Mma {
         for (int r = 0; r < 4; ++r) acc[i][n][r] = 0.f;
   }
   __device__ __forceinline__ void scores(uint32_t kbuf, float (&z)[kOwn][kKeys], float scale, char*, int) {
-    float s[NT][4];
+    float s[NT][4], u[NT][4];                          // two chains of sums
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) s[n][r] = 0.f;
+      for (int r = 0; r < 4; ++r) s[n][r] = u[n][r] = 0.f;
 #pragma unroll
     for (int c = 0; c < HDP / 32; ++c) {
       const uint4 x = lds16(kbuf + (2 * c) * 512), y = lds16(kbuf + (2 * c + 1) * 512);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         mma16816(s[n], x.x, y.x, x.y, y.y, q[c][n][0], q[c][n][1]);
-        mma16816(s[n], x.z, y.z, x.w, y.w, q[c][n][2], q[c][n][3]);
+        mma16816(u[n], x.z, y.z, x.w, y.w, q[c][n][2], q[c][n][3]);
       }
     }
 #pragma unroll
@@ -132,7 +143,7 @@ struct Mma {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) z[2 * n + i][k] = s[n][2 * k + i] * scale;
+        for (int k = 0; k < 2; ++k) z[2 * n + i][k] = (s[n][2 * k + i] + u[n][2 * k + i]) * scale;
   }
   __device__ __forceinline__ void rescale(const float (&corr)[kOwn]) {
 #pragma unroll
@@ -208,14 +219,13 @@ struct Simt {
   float acc[G][kCols][4];
 
   __device__ __forceinline__ static int head(int i, int t) { return G >= 4 ? t * kOwn + i : 0; }
+  static constexpr int kKRows = 1, kVRows = 8 / kRows;
   __device__ __forceinline__ static int k_row(int, int lane) { return lane >> 2; }
-  __device__ __forceinline__ static int k_dim(int c, int lane) { return c * 16 + (lane & 3) * 4; }
-  __device__ __forceinline__ static int v_row(int c, int lane) {
-    return (c / kCols) * kRows + lane / kLanes;
-  }
-  __device__ __forceinline__ static int v_dim(int c, int lane) {
-    return ((c % kCols) * kLanes + lane % kLanes) * 4;
-  }
+  __device__ __forceinline__ static int k_lane(int lane) { return (lane & 3) * 4; }
+  __device__ __forceinline__ static constexpr int k_dim(int c) { return c * 16; }
+  __device__ __forceinline__ static int v_row(int i, int lane) { return i * kRows + lane / kLanes; }
+  __device__ __forceinline__ static int v_lane(int lane) { return lane % kLanes * 4; }
+  __device__ __forceinline__ static constexpr int v_dim(int c) { return (c / kVRows) * kLanes * 4; }
 
   // the block's queries, scaled, in shared memory (every warp writes the same values)
   __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, float scale,
@@ -291,13 +301,13 @@ struct Simt {
     __syncwarp();
     const int sub = lane / kLanes;
 #pragma unroll
-    for (int r = 0; r < 8 / kRows; ++r) {
+    for (int r = 0; r < kVRows; ++r) {
       float w[G];
 #pragma unroll
       for (int h = 0; h < G; ++h) w[h] = s[h * 8 + r * kRows + sub];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        const uint4 x = lds16(vbuf + (r * kCols + c) * 512);
+        const uint4 x = lds16(vbuf + (c * kVRows + r) * 512);
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           acc[h][c][0] = fmaf(w[h], __uint_as_float(x.x), acc[h][c][0]);
@@ -344,37 +354,61 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
   const T* vp = static_cast<const T*>(a.vp);
   const uint32_t buf = sm100::smem_addr(ring) + lane * 16;
   const int32_t* table = a.c.tables + seq * a.c.max_pages;
+  const T* kl = kp + g * a.c.head_stride + E::k_lane(lane);
+  const T* vl = vp + g * a.c.head_stride + E::v_lane(lane);
+  const bool full = hd == E::HDP;
+  const int k_left = hd - E::k_lane(lane), v_left = hd - E::v_lane(lane);
 
-  // a lane looks up the row of one key of a chunk
-  auto page_of = [&](int key) -> int32_t {
-    return key < k1 ? table[static_cast<uint32_t>(key) / static_cast<uint32_t>(a.c.page_size)] : -1;
+  // a lane looks up the row of one key of a chunk: its table entry first, its offset a chunk later
+  struct Entry {
+    int32_t page;
+    uint32_t slot;
   };
-  auto row_of = [&](int key, int32_t page) -> int64_t {
-    if (page < 0 || page >= a.c.n_pages) {
-      if (key < k1) record_device_error(a.c.err, DEVERR_INDEX);
-      return -1;
-    }
-    const uint32_t slot = static_cast<uint32_t>(key) % static_cast<uint32_t>(a.c.page_size);
-    return page * a.c.page_stride + g * a.c.head_stride + slot * a.c.slot_stride;
+  auto entry_of = [&](int key) -> Entry {
+    const uint32_t pi = static_cast<uint32_t>(key) / static_cast<uint32_t>(a.c.page_size);
+    return {key < k1 ? table[pi] : -1, key - pi * static_cast<uint32_t>(a.c.page_size)};
   };
-  auto issue = [&](int64_t row, int s) {          // step s of the chunk whose rows the lanes hold
+  auto row_of = [&](int key, const Entry& x, uint32_t& mask) -> int64_t {
+    const bool in = x.page >= 0 && x.page < a.c.n_pages;
+    if (!in && key < k1) record_device_error(a.c.err, DEVERR_INDEX);
+    mask = __ballot_sync(0xffffffffu, in);
+    return in ? x.page * a.c.page_stride + x.slot * a.c.slot_stride : 0;
+  };
+  // Step s of the chunk whose rows the lanes hold.  Rows without a page are zeros (offset 0 is an
+  // address of the pool, and nothing is read), so are the dims that pad a row.
+  auto issue = [&](int64_t row, uint32_t mask, int s) {
     const uint32_t kb = buf + (s & 1) * 2 * kBuf, vb = kb + kBuf;
+    mask >>= s * E::kStep;
+    {
+      const T* p[E::kKRows];
+      bool in[E::kKRows];
 #pragma unroll
-    for (int c = 0; c < E::kCopies; ++c) {        // (equal rows' exchanges are merged)
-      const int d = E::k_dim(c, lane);
-      const int64_t off = __shfl_sync(0xffffffffu, row, s * E::kStep + E::k_row(c, lane));
-      const bool take = off >= 0 && d < hd;
-      copy16(kb + c * 512, take ? kp + off + d : kp, take);
-    }
-    copy_commit();
+      for (int i = 0; i < E::kKRows; ++i) {
+        const int r = E::k_row(i, lane);
+        p[i] = kl + __shfl_sync(0xffffffffu, row, s * E::kStep + r);
+        in[i] = (mask >> r) & 1u;
+      }
 #pragma unroll
-    for (int c = 0; c < E::kCopies; ++c) {
-      const int d = E::v_dim(c, lane);
-      const int64_t off = __shfl_sync(0xffffffffu, row, s * E::kStep + E::v_row(c, lane));
-      const bool take = off >= 0 && d < hd;
-      copy16(vb + c * 512, take ? vp + off + d : vp, take);
+      for (int c = 0; c < E::kCopies; ++c)
+        copy16(kb + c * 512, p[c % E::kKRows] + E::k_dim(c),
+               in[c % E::kKRows] && (full || E::k_dim(c) < k_left));
+      copy_commit();
     }
-    copy_commit();
+    {
+      const T* p[E::kVRows];
+      bool in[E::kVRows];
+#pragma unroll
+      for (int i = 0; i < E::kVRows; ++i) {
+        const int r = E::v_row(i, lane);
+        p[i] = vl + __shfl_sync(0xffffffffu, row, s * E::kStep + r);
+        in[i] = (mask >> r) & 1u;
+      }
+#pragma unroll
+      for (int c = 0; c < E::kCopies; ++c)
+        copy16(vb + c * 512, p[c % E::kVRows] + E::v_dim(c),
+               in[c % E::kVRows] && (full || E::v_dim(c) < v_left));
+      copy_commit();
+    }
   };
 
   float m[E::kOwn], l[E::kOwn];
@@ -385,33 +419,34 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
 
   int chunk = k0 / kChunk + warp;
   const int end = (k1 + kChunk - 1) / kChunk;
-  int64_t row = -1;
+  int64_t row = 0;
   uint32_t mask = 0;
-  int32_t page = -1;
+  Entry entry{-1, 0};
   if (chunk < end) {
-    row = row_of(chunk * kChunk + lane, page_of(chunk * kChunk + lane));
-    mask = __ballot_sync(0xffffffffu, row >= 0);
-    issue(row, 0);
-    issue(row, 1);
-    if (chunk + W < end) page = page_of((chunk + W) * kChunk + lane);
+    const int key = chunk * kChunk + lane;
+    row = row_of(key, entry_of(key), mask);
+    issue(row, mask, 0);
+    issue(row, mask, 1);
+    if (chunk + W < end) entry = entry_of(key + W * kChunk);
   }
   for (; chunk < end; chunk += W) {
     const bool more = chunk + W < end;
-    int64_t row_n = -1;
+    int64_t row_n = 0;
     uint32_t mask_n = 0;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       const uint32_t kb = buf + (s & 1) * 2 * kBuf;
-      const uint32_t live = (mask >> (s * E::kStep)) & ((1u << E::kStep) - 1u);
+      constexpr uint32_t kAll = (1u << E::kStep) - 1u;
+      const uint32_t live = (mask >> (s * E::kStep)) & kAll;
       copy_wait<3>();                             // this step's keys are there
       if (live) {
         seen = true;
         float z[E::kOwn][E::kKeys];
         e.scores(kb, z, a.scale, bsh, lane);
+        if (a.z != nullptr) {
 #pragma unroll
-        for (int k = 0; k < E::kKeys; ++k) {
-          const bool in = (live >> (g8 + 8 * k)) & 1u;
-          if (a.z != nullptr && in) {
+          for (int k = 0; k < E::kKeys; ++k) {
+            if (!((live >> (g8 + 8 * k)) & 1u)) continue;
             float* zr = a.z + ((seq * a.c.n_kv + g) * a.c.cap + chunk * kChunk + s * E::kStep + g8 + 8 * k) * a.zw;
 #pragma unroll
             for (int i = 0; i < E::kOwn; ++i) {
@@ -419,36 +454,44 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
               if (h < heads && (E::kHeads >= 4 || t == 0)) zr[j0 - g * a.c.group + h] = z[i][k];
             }
           }
-          if (!in) {
-#pragma unroll
-            for (int i = 0; i < E::kOwn; ++i) z[i][k] = -INFINITY;
-          }
         }
-        float corr[E::kOwn], base[E::kOwn];
+        if (live != kAll) {
+#pragma unroll
+          for (int k = 0; k < E::kKeys; ++k)
+            if (!((live >> (g8 + 8 * k)) & 1u)) {
+#pragma unroll
+              for (int i = 0; i < E::kOwn; ++i) z[i][k] = -INFINITY;
+            }
+        }
+        // The scores are taken relative to a maximum that grows only where one exceeds it by more
+        // than 2^kSlack: weights up to 2^kSlack lose nothing in fp32, and most steps need no
+        // exchange between lanes and no rescaling.
         bool grew = false;
 #pragma unroll
-        for (int i = 0; i < E::kOwn; ++i) {
-          float x = z[i][0];
-          if constexpr (E::kKeys == 2) x = fmaxf(x, z[i][1]);
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-          const float mn = fmaxf(m[i], x);
-          grew |= mn > m[i];
-          base[i] = base_of(mn);
-          corr[i] = exp2f(m[i] - base[i]);
-          m[i] = mn;
-        }
-        if (__any_sync(0xffffffffu, grew)) {
-          e.rescale(corr);
+        for (int i = 0; i < E::kOwn; ++i)
 #pragma unroll
-          for (int i = 0; i < E::kOwn; ++i) l[i] *= corr[i];
+          for (int k = 0; k < E::kKeys; ++k) grew |= z[i][k] > m[i] + kSlack;
+        if (__any_sync(0xffffffffu, grew)) {
+          float corr[E::kOwn];
+#pragma unroll
+          for (int i = 0; i < E::kOwn; ++i) {
+            float x = z[i][0];
+            if constexpr (E::kKeys == 2) x = fmaxf(x, z[i][1]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float mn = fmaxf(m[i], x);
+            corr[i] = exp2_f(m[i] - base_of(mn));
+            m[i] = mn;
+            l[i] *= corr[i];
+          }
+          e.rescale(corr);
         }
 #pragma unroll
         for (int i = 0; i < E::kOwn; ++i)
 #pragma unroll
           for (int k = 0; k < E::kKeys; ++k) {
-            z[i][k] = exp2f(z[i][k] - base[i]);
+            z[i][k] = exp2_f(z[i][k] - base_of(m[i]));
             l[i] += z[i][k];
           }
         copy_wait<2>();                           // and its values
@@ -457,15 +500,14 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
       copy_wait<2>();                             // (nothing lands in the slot any more)
       // the ring's slot is free: the step after the next
       if (s + 2 < NS) {
-        issue(row, s + 2);
+        issue(row, mask, s + 2);
       } else {
         if (s + 2 == NS && more) {
           const int key = (chunk + W) * kChunk + lane;
-          row_n = row_of(key, page);
-          mask_n = __ballot_sync(0xffffffffu, row_n >= 0);
-          if (chunk + 2 * W < end) page = page_of(key + W * kChunk);
+          row_n = row_of(key, entry, mask_n);
+          if (chunk + 2 * W < end) entry = entry_of(key + W * kChunk);
         }
-        if (more) issue(row_n, s + 2 - NS);
+        if (more) issue(row_n, mask_n, s + 2 - NS);
         else copy_commit(), copy_commit();
       }
     }
@@ -490,7 +532,7 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
 
 // Weight of a part with maximum pm and sum pl where the joined maximum is m.
 __device__ __forceinline__ float part_weight(float pm, float pl, float m) {
-  return pl == 0.f || pl == -1.f ? 0.f : exp2f(pm - base_of(m));
+  return pl == 0.f || pl == -1.f ? 0.f : exp2_f(pm - base_of(m));
 }
 
 template <typename T>
@@ -668,30 +710,45 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
   }
   const int64_t c0 = u0 / per, c1 = (u1 - 1) / per;
   if (c0 == c1) return;
-  auto slot = [&](int64_t c) { return (2 * c + (c == c0 && u0 > c0 * per ? 1 : 0)) * kHeads + h; };
+  const int parts = static_cast<int>(c1 - c0) + 1;
+  const int64_t slot0 = (2 * c0 + (u0 > c0 * per ? 1 : 0)) * kHeads + h, slot1 = 2 * (c0 + 1) * kHeads + h;
+  auto slot = [&](int c) { return c == 0 ? slot0 : slot1 + (c - 1) * 2 * kHeads; };
+  // every warp finds the common maximum, and its own lanes the weights of the parts
   float mx = -INFINITY;
-  for (int64_t c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, a.pm[slot(c)]);
+  for (int c = lane; c < parts; c += 32) mx = fmaxf(mx, a.pm[slot(c)]);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
   float l = 0.f;
   bool none = false;
   float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
-  for (int64_t c = c0 + warp; c <= c1; c += 4) {
-    const int64_t at = slot(c);
-    const float pl = a.pl[at], w = part_weight(a.pm[at], pl, mx);
-    const bool has = !(pl == 0.f || pl == -1.f);
-    none |= pl == -1.f;
-    if (has) l = fmaf(pl, w, l);
+  for (int b = 0; b < parts; b += 128) {          // warp w: parts b + 32 w .. b + 32 w + 31
+    const int mine = b + warp * 32 + lane;
+    float w = 0.f;
+    if (mine < parts) {
+      const int64_t at = slot(mine);
+      const float pl = a.pl[at];
+      w = part_weight(a.pm[at], pl, mx);
+      none |= pl == -1.f;
+      if (pl != 0.f && pl != -1.f) l = fmaf(pl, w, l);
+    }
+    const int n_here = min(32, parts - b - warp * 32);
+#pragma unroll 8
+    for (int k = 0; k < n_here; ++k) {
+      const int64_t at = slot(b + warp * 32 + k);
+      const float f = __shfl_sync(0xffffffffu, w, k);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int d = (r * 32 + lane) * 4;
-      if (d >= hd || !has) continue;
-      const float4 x = *reinterpret_cast<const float4*>(a.po + at * hd + d);
-      s[r].x = fmaf(x.x, w, s[r].x); s[r].y = fmaf(x.y, w, s[r].y);
-      s[r].z = fmaf(x.z, w, s[r].z); s[r].w = fmaf(x.w, w, s[r].w);
+      for (int r = 0; r < 2; ++r) {
+        const int d = (r * 32 + lane) * 4;
+        if (d >= hd) continue;
+        const float4 x = *reinterpret_cast<const float4*>(a.po + at * hd + d);
+        s[r].x = fmaf(x.x, f, s[r].x); s[r].y = fmaf(x.y, f, s[r].y);
+        s[r].z = fmaf(x.z, f, s[r].z); s[r].w = fmaf(x.w, f, s[r].w);
+      }
     }
   }
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+  none = __any_sync(0xffffffffu, none);
   s_o[warp][lane] = s[0];
   s_o[warp][32 + lane] = s[1];
   if (lane == 0) s_l[warp] = l, s_none[warp] = none;
@@ -722,7 +779,7 @@ static __global__ void __launch_bounds__(256) weights_kernel(const __grid_consta
     if (a.c.at(seq, g, i) < 0) continue;
     const float* z = a.z + (sg * a.c.cap + i) * a.zw;
     float w = 0.f;
-    for (int h = 0; h < a.c.group; ++h) w += exp2f(z[h] - lse[h] * kLog2e);
+    for (int h = 0; h < a.c.group; ++h) w += exp2_f(z[h] - lse[h] * kLog2e);
     a.score[sg * a.c.cap + i] += w;
   }
 }
