@@ -7,9 +7,8 @@
 // What bounds it: every key and value is read once and used by the query heads of its group, a few
 // operations per byte, so the cache's bytes do.  The kernel is built around keeping loads in flight:
 //   * A warp takes 32 keys at a time and stages them itself with 16-byte asynchronous copies into
-//     its own part of shared memory, in the order in which its lanes use them.  Every lane reads
-//     back only what it copied, so there is no barrier and no bank conflict in the loop, and a
-//     page may end anywhere (a row's address is looked up per key, one table entry per lane).
+//     its own part of shared memory, so no warp waits for another in the loop, and a page may end
+//     anywhere (a row's address is looked up per key, one table entry per lane).
 //   * bf16: scores are K q^T and the output V^T p^T with 16 x 8 x 16 matrix instructions, keys or
 //     dims as the rows and the group's heads as the 8 columns, so a group of 8 heads wastes
 //     nothing.  The order of the dims inside a product is free: a lane's 16 bytes of a row are its
@@ -78,6 +77,10 @@ __device__ __forceinline__ float exp2_f(float x) {
 // maximum that scores are taken relative to: an all -infinity maximum gives weights of 0, not NaN
 __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f : m; }
 
+// A staged row is kept with its 16-byte chunks permuted (chunk index xor this): every access below,
+// eight lanes at a time, then touches all banks once.
+__device__ __forceinline__ int swizzle(int row) { return (((row >> 2) ^ row) & 1) << 2 | (row & 2); }
+
 // ---- the two ways to multiply; lane = 4 g + t ----
 // bf16: NT tiles of 8 heads; a step is 16 keys.  A lane's scores: keys g and g + 8, heads
 // 8 nt + 2 t and the next.
@@ -85,24 +88,13 @@ template <int HDP_, int NT>
 struct Mma {
   using T = __nv_bfloat16;
   static constexpr int HDP = HDP_, kHeads = 8 * NT, kStep = 16, kOwn = 2 * NT, kKeys = 2;
-  static constexpr int kCopies = HDP / 16;          // 16-byte copies of a lane, K or V of a step
+  static constexpr int kRowBytes = HDP * 2;
   static constexpr int kShared = 0;                 // block-wide and per-warp scratch
   static constexpr int kWarpShared = 0;
   uint32_t q[HDP / 32][NT][4];
   float acc[HDP / 16][NT][4];
 
   __device__ __forceinline__ static int head(int i, int t) { return (i >> 1) * 8 + 2 * t + (i & 1); }
-  // a lane copies kKRows rows of keys and kVRows of values of a step; copy c is of row c % k?Rows
-  static constexpr int kKRows = 2, kVRows = 4;
-  __device__ __forceinline__ static int k_row(int i, int lane) { return (lane >> 2) + 8 * i; }
-  __device__ __forceinline__ static int k_lane(int lane) { return (lane & 3) * 8; }
-  __device__ __forceinline__ static constexpr int k_dim(int c) { return (c >> 1) * 32; }
-  __device__ __forceinline__ static int v_row(int i, int lane) {
-    return 2 * (lane & 3) + (i & 1) + 8 * (i >> 1);
-  }
-  __device__ __forceinline__ static int v_lane(int lane) { return (lane >> 2) * 8; }
-  __device__ __forceinline__ static constexpr int v_dim(int c) { return (c >> 2) * 64; }
-
   __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, float, char*, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -123,7 +115,11 @@ struct Mma {
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[i][n][r] = 0.f;
   }
-  __device__ __forceinline__ void scores(uint32_t kbuf, float (&z)[kOwn][kKeys], float scale, char*, int) {
+  __device__ __forceinline__ void scores(uint32_t kbuf, float (&z)[kOwn][kKeys], float scale, char*, int lane) {
+    // row g (and g + 8), chunk 4 c + t: the swizzle exchanges even and odd c of a lane
+    const int g = lane >> 2, t = lane & 3, flip = ((g >> 2) ^ g) & 1;
+    const uint32_t at = kbuf + g * kRowBytes + (t ^ (g & 2)) * 16;
+    const uint32_t even = at + flip * 64, odd = at + (flip ^ 1) * 64;
     float s[NT][4], u[NT][4];                          // two chains of sums
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -131,7 +127,8 @@ struct Mma {
       for (int r = 0; r < 4; ++r) s[n][r] = u[n][r] = 0.f;
 #pragma unroll
     for (int c = 0; c < HDP / 32; ++c) {
-      const uint4 x = lds16(kbuf + (2 * c) * 512), y = lds16(kbuf + (2 * c + 1) * 512);
+      const uint32_t k = (c & 1 ? odd : even) + (c & ~1) * 64;
+      const uint4 x = lds16(k), y = lds16(k + 8 * kRowBytes);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         mma16816(s[n], x.x, y.x, x.y, y.y, q[c][n][0], q[c][n][1]);
@@ -156,7 +153,11 @@ struct Mma {
   // The weights enter the product as two bf16 parts, value and remainder (2^-17 of a weight is
   // left): with one part alone the output's error would grow from its own rounding's 0.0017 to
   // about 0.0020, and the second product costs nothing on a stream that memory bounds.
-  __device__ __forceinline__ void add_values(uint32_t vbuf, const float (&p)[kOwn][kKeys], char*, int) {
+  __device__ __forceinline__ void add_values(uint32_t vbuf, const float (&p)[kOwn][kKeys], char*, int lane) {
+    // rows 2 t, 2 t + 1 and 8 further, chunk 8 v + g
+    const int g = lane >> 2, t = lane & 3, sw = ((t & 2) << 1) | ((t & 1) << 1);
+    const uint32_t row0 = vbuf + 2 * t * kRowBytes + (g ^ sw) * 16;
+    const uint32_t row1 = vbuf + (2 * t + 1) * kRowBytes + (g ^ sw ^ 4) * 16;
     uint32_t hi[NT][2], lo[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -172,7 +173,7 @@ struct Mma {
       uint32_t r[4][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint4 x = lds16(vbuf + (4 * v + k) * 512);
+        const uint4 x = lds16((k & 1 ? row1 : row0) + (k >> 1) * 8 * kRowBytes + v * 128);
         r[k][0] = x.x; r[k][1] = x.y; r[k][2] = x.z; r[k][3] = x.w;
       }
 #pragma unroll
@@ -210,7 +211,7 @@ template <int HDP_, int G>
 struct Simt {
   using T = float;
   static constexpr int HDP = HDP_, kHeads = G, kStep = 8, kOwn = G >= 4 ? G / 4 : 1, kKeys = 1;
-  static constexpr int kCopies = HDP / 16;
+  static constexpr int kRowBytes = HDP * 4;
   static constexpr int kShared = G * HDP * 4;
   static constexpr int kWarpShared = 8 * G * 4;
   static constexpr int kLanes = HDP / 4 < 32 ? HDP / 4 : 32;   // lanes of a row of V
@@ -219,14 +220,6 @@ struct Simt {
   float acc[G][kCols][4];
 
   __device__ __forceinline__ static int head(int i, int t) { return G >= 4 ? t * kOwn + i : 0; }
-  static constexpr int kKRows = 1, kVRows = 8 / kRows;
-  __device__ __forceinline__ static int k_row(int, int lane) { return lane >> 2; }
-  __device__ __forceinline__ static int k_lane(int lane) { return (lane & 3) * 4; }
-  __device__ __forceinline__ static constexpr int k_dim(int c) { return c * 16; }
-  __device__ __forceinline__ static int v_row(int i, int lane) { return i * kRows + lane / kLanes; }
-  __device__ __forceinline__ static int v_lane(int lane) { return lane % kLanes * 4; }
-  __device__ __forceinline__ static constexpr int v_dim(int c) { return (c / kVRows) * kLanes * 4; }
-
   // the block's queries, scaled, in shared memory (every warp writes the same values)
   __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, float scale,
                                          char* sq, int lane) {
@@ -246,14 +239,16 @@ struct Simt {
         for (int r = 0; r < 4; ++r) acc[h][c][r] = 0.f;
   }
   __device__ __forceinline__ void scores(uint32_t kbuf, float (&z)[kOwn][kKeys], float, char* sq, int lane) {
-    const int t = lane & 3;
+    const int g = lane >> 2, t = lane & 3, flip = ((g >> 2) ^ g) & 1;
+    const uint32_t at = kbuf + g * kRowBytes + (t ^ (g & 2)) * 16;
+    const uint32_t even = at + flip * 64, odd = at + (flip ^ 1) * 64;
     const uint32_t qa = sm100::smem_addr(sq) + t * 16;
     float s[G];
 #pragma unroll
     for (int h = 0; h < G; ++h) s[h] = 0.f;
 #pragma unroll 4
-    for (int c = 0; c < kCopies; ++c) {
-      const uint4 x = lds16(kbuf + c * 512);
+    for (int c = 0; c < HDP / 16; ++c) {
+      const uint4 x = lds16((c & 1 ? odd : even) + (c & ~1) * 64);
 #pragma unroll
       for (int h = 0; h < G; ++h) {
         const uint4 y = lds16(qa + (h * HDP + c * 16) * 4);
@@ -301,13 +296,15 @@ struct Simt {
     __syncwarp();
     const int sub = lane / kLanes;
 #pragma unroll
-    for (int r = 0; r < kVRows; ++r) {
+    for (int r = 0; r < 8 / kRows; ++r) {
+      const int row = r * kRows + sub;
+      const uint32_t at = vbuf + row * kRowBytes + ((lane % kLanes) ^ swizzle(row)) * 16;
       float w[G];
 #pragma unroll
-      for (int h = 0; h < G; ++h) w[h] = s[h * 8 + r * kRows + sub];
+      for (int h = 0; h < G; ++h) w[h] = s[h * 8 + row];
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
-        const uint4 x = lds16(vbuf + (c * kVRows + r) * 512);
+        const uint4 x = lds16(at + c * kLanes * 16);
 #pragma unroll
         for (int h = 0; h < G; ++h) {
           acc[h][c][0] = fmaf(w[h], __uint_as_float(x.x), acc[h][c][0]);
@@ -335,7 +332,7 @@ struct Simt {
 
 // shared memory of a warp's ring: two steps of keys and values
 template <typename E>
-constexpr int ring_bytes() { return 4 * E::kCopies * 512; }
+constexpr int ring_bytes() { return 4 * E::kStep * E::kRowBytes; }
 template <typename E, int W>
 constexpr int decode_smem() {
   return W * (ring_bytes<E>() + E::kWarpShared) + E::kShared + W * E::kHeads * 8;
@@ -348,16 +345,15 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
                                           int heads, int k0, int k1, char* ring, char* wsh,
                                           char* bsh, float* sm, float* sl, int warp, int lane) {
   using T = typename E::T;
-  constexpr int NS = kChunk / E::kStep, kBuf = E::kCopies * 512;
+  constexpr int NS = kChunk / E::kStep, kBuf = E::kStep * E::kRowBytes, kUnit = 16 / sizeof(T);
   const int t = lane & 3, g8 = lane >> 2, hd = a.c.hd;
   const T* kp = static_cast<const T*>(a.kp);
   const T* vp = static_cast<const T*>(a.vp);
-  const uint32_t buf = sm100::smem_addr(ring) + lane * 16;
+  const uint32_t buf = sm100::smem_addr(ring);
   const int32_t* table = a.c.tables + seq * a.c.max_pages;
-  const T* kl = kp + g * a.c.head_stride + E::k_lane(lane);
-  const T* vl = vp + g * a.c.head_stride + E::v_lane(lane);
-  const bool full = hd == E::HDP;
-  const int k_left = hd - E::k_lane(lane), v_left = hd - E::v_lane(lane);
+  const T* kl = kp + g * a.c.head_stride + (lane & 7) * kUnit;
+  const T* vl = vp + g * a.c.head_stride + (lane & 7) * kUnit;
+  const int left = hd - (lane & 7) * kUnit;      // dims from this lane's first chunk on
 
   // a lane looks up the row of one key of a chunk: its table entry first, its offset a chunk later
   struct Entry {
@@ -376,37 +372,29 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
   };
   // Step s of the chunk whose rows the lanes hold.  Rows without a page are zeros (offset 0 is an
   // address of the pool, and nothing is read), so are the dims that pad a row.
+  // Eight lanes copy 128 consecutive bytes of a row, so that every request is a whole line of L2
+  // (with 32 and 64 bytes of a row to a request the kernel stopped at 4.6 TB/s).
   auto issue = [&](int64_t row, uint32_t mask, int s) {
-    const uint32_t kb = buf + (s & 1) * 2 * kBuf, vb = kb + kBuf;
-    mask >>= s * E::kStep;
-    {
-      const T* p[E::kKRows];
-      bool in[E::kKRows];
+    constexpr int kPtrs = E::kStep / 4, kLines = E::kRowBytes / 128;
+    const int j = lane >> 3;
+    const uint32_t to = buf + (s & 1) * 2 * kBuf + j * E::kRowBytes;
+    const uint32_t to0 = to + ((lane & 7) ^ swizzle(j)) * 16, to1 = to + ((lane & 7) ^ swizzle(j + 4)) * 16;
+    int64_t off[kPtrs];
+    bool in[kPtrs];
+    __syncwarp();                                 // every lane has read what was there
 #pragma unroll
-      for (int i = 0; i < E::kKRows; ++i) {
-        const int r = E::k_row(i, lane);
-        p[i] = kl + __shfl_sync(0xffffffffu, row, s * E::kStep + r);
-        in[i] = (mask >> r) & 1u;
-      }
-#pragma unroll
-      for (int c = 0; c < E::kCopies; ++c)
-        copy16(kb + c * 512, p[c % E::kKRows] + E::k_dim(c),
-               in[c % E::kKRows] && (full || E::k_dim(c) < k_left));
-      copy_commit();
+    for (int i = 0; i < kPtrs; ++i) {
+      off[i] = __shfl_sync(0xffffffffu, row, s * E::kStep + 4 * i + j);
+      in[i] = (mask >> (s * E::kStep + 4 * i + j)) & 1u;
     }
-    {
-      const T* p[E::kVRows];
-      bool in[E::kVRows];
 #pragma unroll
-      for (int i = 0; i < E::kVRows; ++i) {
-        const int r = E::v_row(i, lane);
-        p[i] = vl + __shfl_sync(0xffffffffu, row, s * E::kStep + r);
-        in[i] = (mask >> r) & 1u;
-      }
+    for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll
-      for (int c = 0; c < E::kCopies; ++c)
-        copy16(vb + c * 512, p[c % E::kVRows] + E::v_dim(c),
-               in[c % E::kVRows] && (full || E::v_dim(c) < v_left));
+      for (int i = 0; i < kPtrs; ++i)
+#pragma unroll
+        for (int c = 0; c < kLines; ++c)
+          copy16((i & 1 ? to1 : to0) + kv * kBuf + 4 * i * E::kRowBytes + c * 128,
+                 (kv ? vl : kl) + off[i] + c * 8 * kUnit, in[i] && c * 8 * kUnit < left);
       copy_commit();
     }
   };
@@ -439,6 +427,7 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
       constexpr uint32_t kAll = (1u << E::kStep) - 1u;
       const uint32_t live = (mask >> (s * E::kStep)) & kAll;
       copy_wait<3>();                             // this step's keys are there
+      __syncwarp();
       if (live) {
         seen = true;
         float z[E::kOwn][E::kKeys];
@@ -495,6 +484,7 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
             l[i] += z[i][k];
           }
         copy_wait<2>();                           // and its values
+        __syncwarp();
         e.add_values(kb + kBuf, z, wsh, lane);
       }
       copy_wait<2>();                             // (nothing lands in the slot any more)
