@@ -44,7 +44,7 @@ struct DecodeArgs {
   float* lse;
   float* score;
   // split runs
-  int64_t* first;                // [b + 1]: units before a sequence, of one head tile
+  int64_t* first;                // [b + 2]: units before a sequence, of one head tile; units of a run
   float* pm;                     // [2 * runs][heads of a tile]: maximum (base 2)
   float* pl;                     // ... sum
   float* po;                     // ... [hd]: output before the division
@@ -604,10 +604,15 @@ __global__ void __launch_bounds__(W * 32) decode_whole_kernel(const __grid_const
   block_piece<E, W>(a, e, seq, blockIdx.x / a.tiles, blockIdx.x % a.tiles, 0, n, -1, smem);
 }
 
+// a / b for a >= 0, b > 0; most quotients here fit the quicker 32-bit division
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
 // units per run: at least min_units, so that short work is not cut into parts that cost more to
 // join than to compute
 __device__ __forceinline__ int64_t units_per_run(const DecodeArgs& a, int64_t units) {
-  const int64_t even = (units + a.runs - 1) / a.runs;
+  const int64_t even = quotient(units + a.runs - 1, a.runs);
   return even > a.min_units ? even : a.min_units;
 }
 
@@ -649,7 +654,10 @@ __global__ void __launch_bounds__(W * 32) decode_split_kernel(const __grid_const
       at += chunks(s);
       if (a.c.keys(a.lens, s) != a.lens[s]) record_device_error(a.c.err, DEVERR_INDEX);
     }
-    if (tid == 0) a.first[a.c.b] = total;
+    if (tid == 0) {
+      a.first[a.c.b] = total;
+      a.first[a.c.b + 1] = per;
+    }
   }
   if (u0 >= units) return;
   if (sum > 0 && before * tiles <= u0 && u0 < (before + sum) * tiles) {
@@ -668,7 +676,7 @@ __global__ void __launch_bounds__(W * 32) decode_split_kernel(const __grid_const
       ++seq;
       continue;
     }
-    const int64_t tile = (u - first) / n, begin = first + tile * n;
+    const int64_t tile = quotient(u - first, n), begin = first + tile * n;
     const int64_t stop = min(begin + n, u1);
     const int k0 = static_cast<int>(u - begin) * kChunk;
     const int k1 = static_cast<int>(min((stop - begin) * kChunk, a.c.keys(a.lens, seq)));
@@ -679,17 +687,17 @@ __global__ void __launch_bounds__(W * 32) decode_split_kernel(const __grid_const
   }
 }
 
-// One block per (query head, sequence) that was cut: its parts, in the order of its keys.
+// One block per (query head, sequence) that was cut: its parts, in the order of its keys.  It reads
+// little and waits for what it reads, so everything that one step of 32 parts needs is loaded at
+// once: each lane one part's maximum and sum, each warp eight parts' outputs.
 template <typename T, int kHeads>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ DecodeArgs a) {
   __shared__ float4 s_o[4][64];
-  __shared__ float s_l[4];
-  __shared__ int s_none[4];
   pdl_wait();
   pdl_trigger();
   const int j = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, hd = a.c.hd;
   const int64_t seq = blockIdx.y, tiles = static_cast<int64_t>(a.c.n_kv) * a.tiles;
-  const int64_t f = a.first[seq], n = a.first[seq + 1] - f, per = units_per_run(a, a.first[a.c.b] * tiles);
+  const int64_t f = a.first[seq], n = a.first[seq + 1] - f, per = a.first[a.c.b + 1];
   const int g = j / a.c.group, ht = (j - g * a.c.group) / kHeads, h = (j - g * a.c.group) % kHeads;
   const int64_t u0 = f * tiles + (static_cast<int64_t>(g) * a.tiles + ht) * n, u1 = u0 + n;
   T* o = static_cast<T*>(const_cast<void*>(a.o.p)) + seq * a.o.ts + j * a.o.hs;
@@ -698,53 +706,58 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
     if (tid == 0) a.lse[seq * a.c.n_q + j] = -INFINITY;
     return;
   }
-  const int64_t c0 = u0 / per, c1 = (u1 - 1) / per;
+  const int64_t c0 = quotient(u0, per), c1 = quotient(u1 - 1, per);
   if (c0 == c1) return;
   const int parts = static_cast<int>(c1 - c0) + 1;
   const int64_t slot0 = (2 * c0 + (u0 > c0 * per ? 1 : 0)) * kHeads + h, slot1 = 2 * (c0 + 1) * kHeads + h;
-  auto slot = [&](int c) { return c == 0 ? slot0 : slot1 + (c - 1) * 2 * kHeads; };
-  // every warp finds the common maximum, and its own lanes the weights of the parts
-  float mx = -INFINITY;
-  for (int c = lane; c < parts; c += 32) mx = fmaxf(mx, a.pm[slot(c)]);
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-  float l = 0.f;
+  auto slot = [&](int c) { return c == 0 ? slot0 : slot1 + (c - 1) * (2 * kHeads); };
+  float mx = -INFINITY, l = 0.f;
   bool none = false;
   float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
-  for (int b = 0; b < parts; b += 128) {          // warp w: parts b + 32 w .. b + 32 w + 31
-    const int mine = b + warp * 32 + lane;
-    float w = 0.f;
-    if (mine < parts) {
-      const int64_t at = slot(mine);
-      const float pl = a.pl[at];
-      w = part_weight(a.pm[at], pl, mx);
-      none |= pl == -1.f;
-      if (pl != 0.f && pl != -1.f) l = fmaf(pl, w, l);
+  for (int b = 0; b < parts; b += 32) {
+    float4 x[2][8];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int d = (r * 32 + lane) * 4;
+      if (d >= hd) continue;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = b + warp + 4 * k;
+        if (c < parts) x[r][k] = *reinterpret_cast<const float4*>(a.po + slot(c) * hd + d);
+      }
     }
-    const int n_here = min(32, parts - b - warp * 32);
-#pragma unroll 8
-    for (int k = 0; k < n_here; ++k) {
-      const int64_t at = slot(b + warp * 32 + k);
-      const float f = __shfl_sync(0xffffffffu, w, k);
+    const bool mine = b + lane < parts;
+    const float pm = mine ? a.pm[slot(b + lane)] : -INFINITY, pl = mine ? a.pl[slot(b + lane)] : 0.f;
+    float mn = fmaxf(mx, pm);
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, i));
+    const float keep = exp2_f(mx - base_of(mn)), w = part_weight(pm, pl, mn);
+    mx = mn;
+    none |= pl == -1.f;
+    l = l * keep + (pl == 0.f || pl == -1.f ? 0.f : pl * w);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if ((r * 32 + lane) * 4 >= hd) continue;
+      s[r].x *= keep; s[r].y *= keep; s[r].z *= keep; s[r].w *= keep;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float f = __shfl_sync(0xffffffffu, w, warp + 4 * k);
+      if (b + warp + 4 * k >= parts) continue;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int d = (r * 32 + lane) * 4;
-        if (d >= hd) continue;
-        const float4 x = *reinterpret_cast<const float4*>(a.po + at * hd + d);
-        s[r].x = fmaf(x.x, f, s[r].x); s[r].y = fmaf(x.y, f, s[r].y);
-        s[r].z = fmaf(x.z, f, s[r].z); s[r].w = fmaf(x.w, f, s[r].w);
+        if ((r * 32 + lane) * 4 >= hd) continue;
+        s[r].x = fmaf(x[r][k].x, f, s[r].x); s[r].y = fmaf(x[r][k].y, f, s[r].y);
+        s[r].z = fmaf(x[r][k].z, f, s[r].z); s[r].w = fmaf(x[r][k].w, f, s[r].w);
       }
     }
   }
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-  none = __any_sync(0xffffffffu, none);
+  for (int i = 16; i > 0; i >>= 1) l += __shfl_xor_sync(0xffffffffu, l, i);
+  const float inv = inverse_sum(l, __any_sync(0xffffffffu, none));
   s_o[warp][lane] = s[0];
   s_o[warp][32 + lane] = s[1];
-  if (lane == 0) s_l[warp] = l, s_none[warp] = none;
   __syncthreads();
-  l = s_l[0] + s_l[1] + s_l[2] + s_l[3];
-  const float inv = inverse_sum(l, s_none[0] | s_none[1] | s_none[2] | s_none[3]);
   if (tid * 4 < hd) {
     float4 x = s_o[0][tid];
 #pragma unroll

@@ -64,7 +64,7 @@ DecodeWs decode_ws(const tp::paged::View& c, int dtype, bool with_score) {
   auto take = [&](size_t bytes) { const size_t x = at; at += tp::align256(bytes); return x; };
   const size_t parts = p.whole ? 0 : static_cast<size_t>(2) * p.runs * p.heads;
   w.lse = take(static_cast<size_t>(c.b) * c.n_q * 4);
-  w.first = take(p.whole ? 0 : static_cast<size_t>(c.b + 1) * 8);
+  w.first = take(p.whole ? 0 : static_cast<size_t>(c.b + 2) * 8);
   w.pm = take(parts * 4);
   w.pl = take(parts * 4);
   w.po = take(parts * c.hd * 4);
