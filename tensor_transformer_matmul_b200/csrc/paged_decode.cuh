@@ -552,9 +552,12 @@ __device__ __forceinline__ void block_piece(const DecodeArgs& a, E& e, int64_t s
   const int j0 = g * a.c.group + ht * E::kHeads;
   const int heads = min(E::kHeads, a.c.group - ht * E::kHeads);
   const int hd = a.c.hd;
-  e.load_q(static_cast<const T*>(a.q.p) + seq * a.q.ts + j0 * a.q.hs, a.q.hs, heads, hd, a.scale, bsh, lane);
-  warp_pass<E, W>(a, e, seq, g, j0, heads, k0, k1, ring, wsh, bsh, sm + warp * E::kHeads,
-                  sl + warp * E::kHeads, warp, lane);
+  const int busy = min(W, (k1 - k0 + kChunk - 1) / kChunk);     // warps that get keys
+  if (warp < busy) {
+    e.load_q(static_cast<const T*>(a.q.p) + seq * a.q.ts + j0 * a.q.hs, a.q.hs, heads, hd, a.scale, bsh, lane);
+    warp_pass<E, W>(a, e, seq, g, j0, heads, k0, k1, ring, wsh, bsh, sm + warp * E::kHeads,
+                    sl + warp * E::kHeads, warp, lane);
+  }
   __syncthreads();
   const int cols = hd / 4;
   for (int i = tid; i < heads * cols; i += W * 32) {
@@ -562,11 +565,13 @@ __device__ __forceinline__ void block_piece(const DecodeArgs& a, E& e, int64_t s
     float mx = -INFINITY;
     bool none = false;
 #pragma unroll
-    for (int w = 0; w < W; ++w) mx = fmaxf(mx, sm[w * E::kHeads + h]);
+    for (int w = 0; w < W; ++w)
+      if (w < busy) mx = fmaxf(mx, sm[w * E::kHeads + h]);
     float l = 0.f;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
+      if (w >= busy) break;
       const float pl = sl[w * E::kHeads + h], f = part_weight(sm[w * E::kHeads + h], pl, mx);
       none |= pl == -1.f;
       if (pl == 0.f || pl == -1.f) continue;
@@ -590,6 +595,9 @@ __device__ __forceinline__ void block_piece(const DecodeArgs& a, E& e, int64_t s
   }
   __syncthreads();
 }
+
+// Blocks of a split launch that share an SM (by their rings), and the registers that leaves them.
+constexpr int split_blocks(int hdp) { return hdp == 64 ? 3 : hdp == 128 ? 2 : 1; }
 
 // One block per (head tile, KV head, sequence).
 template <typename E, int W>
@@ -618,7 +626,7 @@ __device__ __forceinline__ int64_t units_per_run(const DecodeArgs& a, int64_t un
 
 // One block per run of units.
 template <typename E, int W>
-__global__ void __launch_bounds__(W * 32) decode_split_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(W * 32, split_blocks(E::HDP)) decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   extern __shared__ __align__(128) char smem[];
   __shared__ int64_t s_sum[W], s_seq, s_first;
   pdl_wait();

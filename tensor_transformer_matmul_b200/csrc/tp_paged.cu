@@ -34,12 +34,9 @@ tp_status check_vec_rows(const tp_head_rows* r, int64_t T, int heads, int hd, in
 tp::rope::Rows rows_of(const tp_head_rows* r) { return {r->data, r->token_stride, r->head_stride}; }
 
 // ---- decode attention: which kernel, and its workspace ----
-// Caches whose rows hold at most this many keys: one block per (sequence, KV head, head tile).
-constexpr int64_t kWholeKeys = 512;
-
 // heads of a tile and blocks of a split launch per SM: of the padded head size and the group
 struct DecodePlan {
-  int hdp, heads, tiles, warps, runs;
+  int hdp, heads, tiles, runs;
   bool whole;
 };
 
@@ -49,8 +46,17 @@ DecodePlan decode_plan(const tp::paged::View& c, int dtype) {
   if (dtype == TP_BF16) p.heads = c.group > 8 && p.hdp < 256 ? 16 : 8;
   else p.heads = c.group == 1 ? 1 : c.group <= 4 ? 4 : 8;
   p.tiles = static_cast<int>(tp::ceil_div(c.group, p.heads));
-  p.whole = c.cap <= kWholeKeys;
-  p.runs = tp::num_sms() * (p.hdp == 64 ? 5 : p.hdp == 128 ? 3 : 1);
+  // One block per (sequence, KV head, head tile) or runs of equal length?  A block alone streams
+  // about 0.1 TB/s; a split launch costs about 7 us more (the cuts' joins, a second kernel) but no
+  // row, however long, then holds the others up.  The host knows the rows' room, not their lengths,
+  // so whole rows are for room that one block reads in 10 us, or in 25 us where there are enough
+  // blocks to keep a third of the SMs busy.  Measured on 64 / 8 bf16 heads of 128 dims, whole and
+  // split: 1 x 700 keys 7.3 / 10.2 us, 1 x 4000 24.8 / 14.2, 16 ragged up to 1500 14.8 / 21.8,
+  // 16 up to 4096 29.6 / 35.2, 64 up to 700 26 / 40, 16 up to 8000 56 / 58.
+  const int64_t blocks = c.b * c.n_kv * p.tiles;
+  const int64_t row = c.cap * c.hd * 2 * tp::elem_bytes(dtype);
+  p.whole = row <= (3 << 18) || (row <= (5 << 19) && blocks * 3 >= tp::num_sms());
+  p.runs = tp::num_sms() * tp::paged::split_blocks(p.hdp);
   return p;
 }
 
@@ -76,7 +82,7 @@ DecodeWs decode_ws(const tp::paged::View& c, int dtype, bool with_score) {
 template <typename E>
 tp_status launch_decode(const tp::paged::DecodeArgs& a, const DecodePlan& p, cudaStream_t s) {
   using namespace tp::paged;
-  constexpr int kWhole = E::HDP == 256 ? 4 : 8, kSplit = E::HDP == 256 ? 6 : 4;
+  constexpr int kWhole = E::HDP == 256 ? 6 : 12, kSplit = 6;
   const int smem = p.whole ? decode_smem<E, kWhole>() : decode_smem<E, kSplit>();
   auto* whole = decode_whole_kernel<E, kWhole>;
   auto* split = decode_split_kernel<E, kSplit>;
