@@ -48,7 +48,7 @@ struct DecodeArgs {
   float* pm;                     // [2 * runs][heads of a tile]: maximum (base 2)
   float* pl;                     // ... sum
   float* po;                     // ... [hd]: output before the division
-  float* z;                      // [b][n_kv][cap][zw]: base-2 scores, for the weights
+  float* z;                      // [b][n_kv][cap][zw]: base-2 scores, for the weights (may be null)
   int64_t min_units;
   int runs, tiles, zw;           // blocks; head tiles of a group; columns of z
 };
@@ -67,6 +67,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+constexpr uint32_t kLeftOut = 0x7fc0dead;   // in place of a score: a NaN that no operation returns
 constexpr float kSlack = 8.f;
 // 2^x by the hardware's instruction (relative error 2^-22; results below 2^-126 are zeros)
 __device__ __forceinline__ float exp2_f(float x) {
@@ -141,6 +142,14 @@ struct Mma {
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k) z[2 * n + i][k] = (s[n][2 * k + i] + u[n][2 * k + i]) * scale;
+  }
+  // key k's scores into its row (columns behind the group's last head hold anything)
+  __device__ __forceinline__ static void keep_scores(float* to, const float (&z)[kOwn][kKeys], int k,
+                                                     int t, int room) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (8 * n + 2 * t < room)
+        *reinterpret_cast<float2*>(to + 8 * n + 2 * t) = make_float2(z[2 * n][k], z[2 * n + 1][k]);
   }
   __device__ __forceinline__ void rescale(const float (&corr)[kOwn]) {
 #pragma unroll
@@ -277,6 +286,12 @@ struct Simt {
       }
     }
   }
+  __device__ __forceinline__ static void keep_scores(float* to, const float (&z)[kOwn][kKeys], int k,
+                                                     int t, int room) {
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+      if (head(i, t) < room && (G >= 4 || t == 0)) to[head(i, t)] = z[i][k];
+  }
   __device__ __forceinline__ void rescale(const float (&corr)[kOwn]) {
 #pragma unroll
     for (int h = 0; h < G; ++h) {
@@ -355,6 +370,11 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
   const T* vl = vp + g * a.c.head_stride + (lane & 7) * kUnit;
   const int left = hd - (lane & 7) * kUnit;      // dims from this lane's first chunk on
 
+  // a key's scores, from this tile's heads on; columns left there
+  const int room = a.zw - (j0 - g * a.c.group);
+  auto z_row = [&](int key) {
+    return a.z + ((seq * a.c.n_kv + g) * a.c.cap + key) * a.zw + (j0 - g * a.c.group);
+  };
   // a lane looks up the row of one key of a chunk: its table entry first, its offset a chunk later
   struct Entry {
     int32_t page;
@@ -434,15 +454,8 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
         e.scores(kb, z, a.scale, bsh, lane);
         if (a.z != nullptr) {
 #pragma unroll
-          for (int k = 0; k < E::kKeys; ++k) {
-            if (!((live >> (g8 + 8 * k)) & 1u)) continue;
-            float* zr = a.z + ((seq * a.c.n_kv + g) * a.c.cap + chunk * kChunk + s * E::kStep + g8 + 8 * k) * a.zw;
-#pragma unroll
-            for (int i = 0; i < E::kOwn; ++i) {
-              const int h = E::head(i, t);
-              if (h < heads && (E::kHeads >= 4 || t == 0)) zr[j0 - g * a.c.group + h] = z[i][k];
-            }
-          }
+          for (int k = 0; k < E::kKeys; ++k)
+            if ((live >> (g8 + 8 * k)) & 1u) e.keep_scores(z_row(chunk * kChunk + s * E::kStep + g8 + 8 * k), z, k, t, room);
         }
         if (live != kAll) {
 #pragma unroll
@@ -488,6 +501,10 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
         e.add_values(kb + kBuf, z, wsh, lane);
       }
       copy_wait<2>();                             // (nothing lands in the slot any more)
+      if (a.z != nullptr && live != kAll && lane < E::kStep && !((live >> lane) & 1u)) {
+        const int key = chunk * kChunk + s * E::kStep + lane;
+        if (key < k1) *z_row(key) = __uint_as_float(kLeftOut);
+      }
       // the ring's slot is free: the step after the next
       if (s + 2 < NS) {
         issue(row, mask, s + 2);
@@ -536,6 +553,46 @@ __device__ __forceinline__ void store4(T* p, float a, float b, float c, float d)
 // 1 / l of a joined sum; none < 0: keys without a softmax (NaN), no keys at all: 0
 __device__ __forceinline__ float inverse_sum(float l, bool none) {
   return l == 0.f ? (none ? NAN : 0.f) : 1.f / l;
+}
+
+// The weights that the group's heads gave to keys first, first + stride, ...: 2^(z - lse), heads in
+// order.  s_lse: base-2 values of the first kWeightHeads heads (lse has all, natural).
+constexpr int kWeightHeads = 64;
+__device__ __forceinline__ void add_weights(const DecodeArgs& a, int64_t seq, int g, int n,
+                                            const float* s_lse, const float* lse, int first, int stride) {
+  constexpr int kKeys = 4;       // keys of a thread whose loads fly together
+  const int64_t row = (seq * a.c.n_kv + g) * a.c.cap;
+  for (int i0 = first; i0 < n; i0 += kKeys * stride) {
+    float w[kKeys], old[kKeys];
+    bool take[kKeys];
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k) {
+      take[k] = i0 + k * stride < n;
+      w[k] = 0.f;
+      old[k] = take[k] ? a.score[row + i0 + k * stride] : 0.f;
+    }
+#pragma unroll 2
+    for (int h = 0; h < a.c.group; h += 4) {
+      float4 x[kKeys];
+#pragma unroll
+      for (int k = 0; k < kKeys; ++k)
+        if (i0 + k * stride < n)
+          x[k] = *reinterpret_cast<const float4*>(a.z + (row + i0 + k * stride) * a.zw + h);
+#pragma unroll
+      for (int k = 0; k < kKeys; ++k) {
+        if (!take[k]) continue;
+        if (h == 0) take[k] = __float_as_uint(x[k].x) != kLeftOut;
+        const float v[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (h + r < a.c.group)
+            w[k] += exp2_f(v[r] - (h + r < kWeightHeads ? s_lse[h + r] : lse[h + r] * kLog2e));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kKeys; ++k)
+      if (take[k]) a.score[row + i0 + k * stride] = old[k] + w[k];
+  }
 }
 
 // Joins the warps' parts of keys k0 .. k1-1 and writes the output (slot < 0) or a part.
@@ -609,7 +666,16 @@ __global__ void __launch_bounds__(W * 32) decode_whole_kernel(const __grid_const
   const int n = static_cast<int>(a.c.keys(a.lens, seq));
   if (blockIdx.x == 0 && threadIdx.x == 0 && n != a.lens[seq]) record_device_error(a.c.err, DEVERR_INDEX);
   E e;
-  block_piece<E, W>(a, e, seq, blockIdx.x / a.tiles, blockIdx.x % a.tiles, 0, n, -1, smem);
+  const int g = blockIdx.x / a.tiles;
+  block_piece<E, W>(a, e, seq, g, blockIdx.x % a.tiles, 0, n, -1, smem);
+  // the scores that this block left behind, as weights, where it has all heads of the group
+  if (a.z != nullptr && a.tiles == 1) {
+    const float* lse = a.lse + seq * a.c.n_q + g * a.c.group;
+    float* s_lse = reinterpret_cast<float*>(smem);
+    if (threadIdx.x < a.c.group) s_lse[threadIdx.x] = lse[threadIdx.x] * kLog2e;
+    __syncthreads();
+    add_weights(a, seq, g, n, s_lse, lse, threadIdx.x, W * 32);
+  }
 }
 
 // a / b for a >= 0, b > 0; most quotients here fit the quicker 32-bit division
@@ -778,21 +844,18 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
   if (tid == 0) a.lse[seq * a.c.n_q + j] = fmaf(mx, kLn2, logf(l));
 }
 
-// score += the group's weights of each key, heads in order.
+// score += the group's weights of each key, for the cut rows and the tiled groups.
 static __global__ void __launch_bounds__(256) weights_kernel(const __grid_constant__ DecodeArgs a) {
+  __shared__ float s_lse[kWeightHeads];
   pdl_wait();
   pdl_trigger();
   const int g = blockIdx.y;
-  const int64_t seq = blockIdx.z, sg = seq * a.c.n_kv + g;
+  const int64_t seq = blockIdx.z;
   const int n = static_cast<int>(a.c.keys(a.lens, seq));
   const float* lse = a.lse + seq * a.c.n_q + g * a.c.group;
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
-    if (a.c.at(seq, g, i) < 0) continue;
-    const float* z = a.z + (sg * a.c.cap + i) * a.zw;
-    float w = 0.f;
-    for (int h = 0; h < a.c.group; ++h) w += exp2_f(z[h] - lse[h] * kLog2e);
-    a.score[sg * a.c.cap + i] += w;
-  }
+  for (int h = threadIdx.x; h < min(a.c.group, kWeightHeads); h += 256) s_lse[h] = lse[h] * kLog2e;
+  __syncthreads();
+  add_weights(a, seq, g, n, s_lse, lse, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }
 
 }  // namespace paged

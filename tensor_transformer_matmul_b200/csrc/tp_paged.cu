@@ -60,6 +60,9 @@ DecodePlan decode_plan(const tp::paged::View& c, int dtype) {
   return p;
 }
 
+// columns of a key's kept scores: the group's heads, in 16-byte vectors
+int score_columns(const tp::paged::View& c) { return static_cast<int>(tp::round_up(c.group, 4)); }
+
 struct DecodeWs {
   size_t lse, first, pm, pl, po, z, total;
 };
@@ -74,7 +77,7 @@ DecodeWs decode_ws(const tp::paged::View& c, int dtype, bool with_score) {
   w.pm = take(parts * 4);
   w.pl = take(parts * 4);
   w.po = take(parts * c.hd * 4);
-  w.z = take(with_score ? static_cast<size_t>(c.b) * c.n_q * c.cap * 4 : 0);
+  w.z = take(with_score ? static_cast<size_t>(c.b) * c.n_kv * c.cap * score_columns(c) * 4 : 0);
   w.total = at;
   return w;
 }
@@ -272,7 +275,7 @@ extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_he
   a.pl = reinterpret_cast<float*>(ws + w.pl);
   a.po = reinterpret_cast<float*>(ws + w.po);
   a.z = score ? reinterpret_cast<float*>(ws + w.z) : nullptr;
-  a.zw = a.c.group;
+  a.zw = score_columns(a.c);
   a.tiles = p.tiles;
   a.runs = p.runs;
   a.min_units = 4;
@@ -288,9 +291,9 @@ extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_he
                                       : launch_decode<Simt<H, 8>>(a, p, s)))
   st = p.hdp == 64 ? TP_DECODE(64) : p.hdp == 128 ? TP_DECODE(128) : TP_DECODE(256);
 #undef TP_DECODE
-  if (st != TP_OK || !score) return st;
+  if (st != TP_OK || !score || (p.whole && p.tiles == 1)) return st;
   tp::ProfScope prof(s, "attn_score_paged");
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tp::ceil_div(a.c.cap, 256), 256)),
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tp::ceil_div(a.c.cap, 512), 256)),
                   static_cast<unsigned>(desc->n_kv), static_cast<unsigned>(desc->b));
   TP_LAUNCH_PDL(tp::paged::weights_kernel, grid, dim3(256), 0, s, a);
   return TP_OK;
