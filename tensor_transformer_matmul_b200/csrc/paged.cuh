@@ -121,7 +121,7 @@ struct EvictArgs {
   int32_t* keep;        // [b][n_kv][budget]
   int32_t* cut;         // [b][n_kv]: 1 where the sequence is longer than the budget
   int32_t* new_ws;      // [b]
-  int budget, recent;
+  int budget, recent, room, strips;
   void *kp, *vp;
 };
 
@@ -132,10 +132,11 @@ __device__ __forceinline__ uint32_t rank_of(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-constexpr int kEvictThreads = 1024;
+constexpr int kEvictThreads = 1024, kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictRoom = 50000;      // scores that a block keeps in shared memory
 
-// exclusive sum over the block's threads; *total gets the whole
-__device__ __forceinline__ int block_scan(int v, int* total, int* s_warp) {
+// Sum over the threads before this one; s_warp: kEvictWarps ints.
+__device__ __forceinline__ int sum_before(int v, int* s_warp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int x = v;
 #pragma unroll
@@ -145,38 +146,32 @@ __device__ __forceinline__ int block_scan(int v, int* total, int* s_warp) {
   }
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    const int nw = blockDim.x >> 5;
-    int w = lane < nw ? s_warp[lane] : 0;
+  int w = s_warp[lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += y;
-    }
-    if (lane < nw) s_warp[lane] = w;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, w, o);
+    if (lane >= o) w += y;
   }
-  __syncthreads();
-  *total = s_warp[(blockDim.x >> 5) - 1];
-  const int before = warp > 0 ? s_warp[warp - 1] : 0;
-  __syncthreads();
-  return before + x - v;
+  return (warp > 0 ? __shfl_sync(0xffffffffu, w, warp - 1) : 0) + x - v;
 }
 
-// One block per (KV head, sequence): the budget-recent largest scores by a radix search of the
-// threshold (8 bits a pass, counted in shared memory), then their slots in order, ties from the
-// lowest; the kept scores move down in chunks (a chunk is read before it is written, and a kept
-// score never moves up).
-static __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  __shared__ int s_hist[256], s_warp[32];
+// One block per (KV head, sequence).  The scores are read once into shared memory (rows longer than
+// kEvictRoom: from L2 each time).  Three passes find the smallest score that stays, by 12, 10 and 10
+// bits: counts by digit (12 bits spread the scores' few octaves over enough counters), and a sum
+// over the digits from above.  Then every warp has a run of slots: it counts what stays of it, and
+// with the counts before it writes the kept slots in order, of the scores equal to the smallest the
+// first ones.  Bound by the latency of its steps; the rows it selects cost far more to move.
+static __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
+  extern __shared__ float s_score[];
+  __shared__ int s_hist[4096 + 2 * 1024], s_warp[3][kEvictWarps], s_above[kEvictWarps], s_ties[kEvictWarps];
   __shared__ uint32_t s_prefix;
   __shared__ int s_want;
-  const int g = blockIdx.x, tid = threadIdx.x;
+  pdl_wait();
+  pdl_trigger();
+  const int g = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t seq = blockIdx.y, sg = seq * a.c.n_kv + g;
-  const int64_t n64 = a.c.keys(a.lens, seq);
-  if (tid == 0 && n64 != a.lens[seq]) record_device_error(a.c.err, DEVERR_INDEX);
-  const int n = static_cast<int>(n64), budget = a.budget;
+  const int n = static_cast<int>(a.c.keys(a.lens, seq)), budget = a.budget;
+  if (tid == 0 && n != a.lens[seq]) record_device_error(a.c.err, DEVERR_INDEX);
   float* score = a.score + sg * a.c.cap;
   int32_t* keep = a.keep + sg * budget;
   int32_t* out = a.keep_out ? a.keep_out + sg * budget : nullptr;
@@ -186,96 +181,205 @@ static __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(Evic
   }
   if (n <= budget) {
     if (out)
-      for (int i = tid; i < budget; i += blockDim.x) out[i] = i < n ? i : -1;
+      for (int i = tid; i < budget; i += kEvictThreads) out[i] = i < n ? i : -1;
     return;
   }
   const int old = n - a.recent;             // candidates: slots 0 .. old-1
   const int pick = budget - a.recent;       // how many of them stay (< old)
+  const bool held = n <= a.room;
+  for (int i = tid; i < 4096 + 2 * 1024; i += kEvictThreads) s_hist[i] = 0;
+  if (held)
+    for (int i = tid; i < n; i += kEvictThreads) s_score[i] = score[i];
+  const float* from = held ? s_score : score;
+  __syncthreads();
   uint32_t prefix = 0;
   int want = pick;
   if (pick > 0) {
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += blockDim.x) s_hist[i] = 0;
-      __syncthreads();
-      const uint32_t mask = shift == 24 ? 0u : 0xffffffffu << (shift + 8);
-      for (int i = tid; i < old; i += blockDim.x) {
-        const uint32_t u = rank_of(score[i]);
-        if ((u & mask) == prefix) atomicAdd(&s_hist[(u >> shift) & 255], 1);
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+      constexpr int kShift[3] = {20, 10, 0}, kFirst[3] = {0, 4096, 4096 + 1024};
+      const int shift = kShift[p], per = p == 0 ? 4 : 1;
+      const uint32_t digits = p == 0 ? 4096 : 1024, mask = p == 0 ? 0u : 0xffffffffu << (p == 1 ? 20 : 10);
+      int* hist = s_hist + kFirst[p];
+      for (int i0 = warp * 32; i0 < old; i0 += kEvictThreads) {
+        const int i = i0 + lane;
+        const uint32_t u = i < old ? rank_of(from[i]) : 0u;
+        const bool in = i < old && (u & mask) == prefix;
+        const uint32_t d = in ? (u >> shift) & (digits - 1) : digits;
+        int same;
+        __match_all_sync(0xffffffffu, d, &same);       // equal scores: one count for the warp
+        if (in && (!same || lane == 0)) atomicAdd(&hist[d], same ? 32 : 1);
       }
       __syncthreads();
-      if (tid == 0) {
-        int left = want, d = 255;
-        while (d > 0 && s_hist[d] < left) left -= s_hist[d--];
-        s_prefix = prefix | (static_cast<uint32_t>(d) << shift);
-        s_want = left;
+      // this thread's digits, from above; the one whose sum from above reaches ``want``
+      int c[4], sum = 0;
+      const int top = static_cast<int>(digits) - 1 - tid * per;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k < per) sum += c[k] = hist[top - k];
+      int before = sum_before(sum, s_warp[p]);
+      if (before < want && before + sum >= want) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (k >= per) break;
+          if (before < want && before + c[k] >= want) {
+            s_prefix = prefix | static_cast<uint32_t>(top - k) << shift;
+            s_want = want - before;
+          }
+          before += c[k];
+        }
       }
       __syncthreads();
       prefix = s_prefix;
       want = s_want;
-      __syncthreads();
     }
   }
   // above the threshold: all; equal to it: the first ``want`` by slot
-  int kept = 0, ties = 0;
-  for (int i0 = 0; i0 < old && pick > 0; i0 += blockDim.x) {
-    const int i = i0 + tid;
-    const uint32_t u = i < old ? rank_of(score[i]) : 0u;
-    const int tie = i < old && u == prefix;
-    int n_tie, n_keep;
-    const int t = ties + block_scan(tie, &n_tie, s_warp);
-    const int k = i < old && (u > prefix || (tie && t < want));
-    const int at = kept + block_scan(k, &n_keep, s_warp);
-    if (k) keep[at] = i;
-    ties += n_tie;
-    kept += n_keep;
+  const int run = (old + kEvictThreads - 1) / kEvictThreads * 32, begin = min(warp * run, old),
+            end = min(begin + run, old);
+  int above = 0, ties = 0;
+  for (int i = begin + lane; i < end; i += 32) {
+    const uint32_t u = rank_of(from[i]);
+    above += u > prefix;
+    ties += u == prefix;
   }
-  for (int i = tid; i < a.recent; i += blockDim.x) keep[pick + i] = old + i;
+  above = __reduce_add_sync(0xffffffffu, above);
+  ties = __reduce_add_sync(0xffffffffu, ties);
+  if (lane == 0) s_above[warp] = above, s_ties[warp] = ties;
   __syncthreads();
-  for (int j0 = 0; j0 < budget; j0 += blockDim.x) {
-    const int j = j0 + tid;
-    float v = 0.f;
-    int from = 0;
-    if (j < budget) {
-      from = keep[j];
-      v = score[from];
-      if (out) out[j] = from;
+  int at = 0, tie = 0;
+  for (int w = 0; w < warp; ++w) at += s_above[w], tie += s_ties[w];
+  at += min(tie, want);
+  for (int i0 = begin; i0 < end && pick > 0; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t u = i < end ? rank_of(from[i]) : 0u;
+    const uint32_t same = __ballot_sync(0xffffffffu, i < end && u == prefix), below = (1u << lane) - 1u;
+    const bool stays = i < end && (u > prefix || (u == prefix && tie + __popc(same & below) < want));
+    const uint32_t all = __ballot_sync(0xffffffffu, stays);
+    if (stays) {
+      const int j = at + __popc(all & below);
+      keep[j] = i;
+      if (out) out[j] = i;
+      if (held) score[j] = from[i];
     }
+    at += __popc(all);
+    tie += __popc(same);
+  }
+  for (int i = tid; i < a.recent; i += kEvictThreads) {
+    keep[pick + i] = old + i;
+    if (out) out[pick + i] = old + i;
+    if (held) score[pick + i] = from[old + i];
+  }
+  if (held) return;
+  // the kept scores move down in place: a kept score never moves up, and what a step writes was
+  // read by it or by an earlier one
+  __syncthreads();
+  for (int j0 = 0; j0 < budget; j0 += kEvictThreads) {
+    const int j = j0 + tid;
+    const float v = j < budget ? score[keep[j]] : 0.f;
     __syncthreads();
     if (j < budget) score[j] = v;
+    __syncthreads();
   }
 }
 
-// One block per (16-byte column pair of K or V, KV head, sequence): the kept rows' columns move
-// down chunk by chunk.  Row j comes from slot keep[j] >= j, so rows written by earlier chunks are
-// never read again, and a chunk is read before it is written.
-static __global__ void __launch_bounds__(256) evict_move_kernel(EvictArgs a, int eb) {
+// One warp per (KV head, sequence, K or V, 128-byte strip of a row): the kept rows' strips move down
+// in place through a ring of kDepth chunks of 32 rows in shared memory.  Row j comes from slot
+// keep[j] >= j: a chunk is written once it and all before it were read, and rows that were written
+// are never read again, so reading ahead needs nothing but that order, and no warp waits for
+// another.  Bound by the bytes: each kept row is read and written once, by whole lines of L2.
+template <int kDepth>
+__global__ void __launch_bounds__(32) evict_move_kernel(const __grid_constant__ EvictArgs a, int eb) {
+  extern __shared__ __align__(128) char smem[];
   pdl_wait();
   pdl_trigger();
-  const int g = blockIdx.y, tid = threadIdx.x;
+  const int lane = threadIdx.x, part = blockIdx.x, g = blockIdx.y;
   const int64_t seq = blockIdx.z, sg = seq * a.c.n_kv + g;
-  const int units = a.c.hd * eb / 16;                 // 16-byte columns of a row
-  if (blockIdx.x == 0 && g == 0 && tid == 0) a.new_lens[seq] = a.new_ws[seq];
+  if (part == 0 && g == 0 && lane == 0) a.new_lens[seq] = a.new_ws[seq];
   if (!a.cut[sg]) return;
   const int32_t* keep = a.keep + sg * a.budget;
-  char* base = static_cast<char*>(blockIdx.x < units ? a.kp : a.vp);
-  const int col = (blockIdx.x % units) * 16;
-  for (int j0 = 0; j0 < a.budget; j0 += 256) {
-    const int j = j0 + tid;
-    uint4 x;
-    int64_t to = -1;
-    if (j < a.budget && keep[j] != j) {
-      const int64_t from = a.c.at(seq, g, keep[j]);
-      to = a.c.at(seq, g, j);
-      if (from < 0 || to < 0) {
-        record_device_error(a.c.err, DEVERR_INDEX);
-        to = -1;
-      } else {
-        x = *reinterpret_cast<const uint4*>(base + from * eb + col);
-      }
+  const int32_t* table = a.c.tables + seq * a.c.max_pages;
+  const int col = (part >> 1) * 128 + (lane & 7) * 16, sub = lane >> 3, budget = a.budget;
+  char* base = static_cast<char*>(part & 1 ? a.vp : a.kp) + g * a.c.head_stride * eb + col;
+  const bool mine = col < a.c.hd * eb;
+  const uint32_t ring = sm100::smem_addr(smem) + lane * 16;
+  int64_t* s_to = reinterpret_cast<int64_t*>(smem + kDepth * 4096);    // [kDepth][32] byte offsets
+  const int chunks = (budget + 31) / 32;
+  const uint32_t page_size = static_cast<uint32_t>(a.c.page_size);
+  auto offset = [&](int slot, int32_t page) -> int64_t {
+    const int in = slot - static_cast<int>(static_cast<uint32_t>(slot) / page_size * page_size);
+    return (page * a.c.page_stride + in * a.c.slot_stride) * eb;
+  };
+  auto valid = [&](int32_t page) { return page >= 0 && page < a.c.n_pages; };
+  // The lookups of four chunks at once, two and one turns of the loop ahead of their use: a lane's
+  // slots first, then the pages of where its rows come from and go.
+  struct Rows4 {
+    int slot[4];
+    int32_t from[4], to[4];
+  };
+  auto load_slots = [&](int c, Rows4& x) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = (c + k) * 32 + lane;
+      x.slot[k] = j < budget ? keep[j] : -1;
     }
-    __syncthreads();
-    if (to >= 0) *reinterpret_cast<uint4*>(base + to * eb + col) = x;
+  };
+  auto load_pages = [&](int c, Rows4& x) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int j = (c + k) * 32 + lane;
+      const bool moves = x.slot[k] > j;                // (a row that stays is left alone)
+      x.from[k] = moves ? table[static_cast<uint32_t>(x.slot[k]) / page_size] : 0;
+      x.to[k] = moves ? table[static_cast<uint32_t>(j) / page_size] : 0;
+    }
+  };
+  Rows4 now, next;
+  load_slots(0, now);
+  load_pages(0, now);
+  load_slots(4, next);
+#pragma unroll 1
+  for (int c = 0; c < chunks + kDepth; c += 4) {
+    Rows4 after;
+    load_slots(c + 8, after);
+    load_pages(c + 4, next);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int in = c + k, out = in - kDepth, j = in * 32 + lane;
+      const uint32_t at = ring + (in % kDepth) * 4096;
+      int64_t* to = s_to + (in % kDepth) * 32;
+      if (out >= 0 && out < chunks) {
+        copy_wait<kDepth - 1>();
+        __syncwarp();                     // all lanes' copies of this chunk have landed
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t row = to[4 * i + sub];
+          if (row >= 0 && mine) *reinterpret_cast<uint4*>(base + row) = lds16(at + i * 512);
+        }
+        __syncwarp();
+      }
+      if (in < chunks) {
+        int64_t from = -1, dest = -1;
+        if (now.slot[k] > j) {
+          if (valid(now.from[k]) && valid(now.to[k])) {
+            from = offset(now.slot[k], now.from[k]);
+            dest = offset(j, now.to[k]);
+          } else {
+            record_device_error(a.c.err, DEVERR_INDEX);
+          }
+        }
+        to[lane] = dest;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int64_t row = __shfl_sync(0xffffffffu, from, 4 * i + sub);
+          if (row >= 0 && mine) copy16(at + i * 512, base + row, true);
+        }
+      }
+      copy_commit();
+    }
+    now = next;
+    next = after;
   }
+  copy_wait<0>();
 }
 
 }  // namespace paged

@@ -347,18 +347,32 @@ extern "C" tp_status tp_kv_evict_paged(const tp_paged_desc* desc, void* score, c
   a.recent = recent;
   a.kp = k_pages;
   a.vp = v_pages;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int eb = tp::elem_bytes(desc->dtype);
+  a.room = static_cast<int>(std::min<int64_t>(a.c.cap, tp::paged::kEvictRoom));
+  a.strips = static_cast<int>(tp::ceil_div(static_cast<int64_t>(desc->head_dim) * eb, 128));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   {
     tp::ProfScope prof(s, "kv_evict_select");
+    const int smem = a.room * 4;
+    TP_CUDA_TRY(cudaFuncSetAttribute(tp::paged::evict_select_kernel,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     TP_LAUNCH_PDL(tp::paged::evict_select_kernel,
                   dim3(static_cast<unsigned>(desc->n_kv), static_cast<unsigned>(desc->b)),
-                  dim3(tp::paged::kEvictThreads), 0, s, a);
+                  dim3(tp::paged::kEvictThreads), smem, s, a);
   }
   tp::ProfScope prof(s, "kv_evict_move");
-  TP_LAUNCH_PDL(tp::paged::evict_move_kernel,
-                dim3(static_cast<unsigned>(2 * desc->head_dim * eb / 16),
-                     static_cast<unsigned>(desc->n_kv), static_cast<unsigned>(desc->b)),
-                dim3(256), 0, s, a, eb);
+  const dim3 grid(static_cast<unsigned>(2 * a.strips), static_cast<unsigned>(desc->n_kv),
+                  static_cast<unsigned>(desc->b));
+  // few warps: deep rings, so that each alone has enough in flight
+  const int64_t warps = static_cast<int64_t>(grid.x) * grid.y * grid.z;
+#define TP_MOVE(D)                                                                            \
+  do {                                                                                        \
+    TP_CUDA_TRY(cudaFuncSetAttribute(tp::paged::evict_move_kernel<D>,                         \
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, D * 4352)); \
+    TP_LAUNCH_PDL(tp::paged::evict_move_kernel<D>, grid, dim3(32), D * 4352, s, a, eb);       \
+  } while (0)
+  if (warps <= 3 * tp::num_sms()) TP_MOVE(16);
+  else TP_MOVE(6);
+#undef TP_MOVE
   return TP_OK;
 }
