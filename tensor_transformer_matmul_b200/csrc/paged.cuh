@@ -188,8 +188,17 @@ static __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(cons
   const int pick = budget - a.recent;       // how many of them stay (< old)
   const bool held = n <= a.room;
   for (int i = tid; i < 4096 + 2 * 1024; i += kEvictThreads) s_hist[i] = 0;
-  if (held)
-    for (int i = tid; i < n; i += kEvictThreads) s_score[i] = score[i];
+  if (held) {
+    for (int i0 = tid; i0 < n; i0 += 8 * kEvictThreads) {
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i0 + k * kEvictThreads < n) x[k] = score[i0 + k * kEvictThreads];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (i0 + k * kEvictThreads < n) s_score[i0 + k * kEvictThreads] = x[k];
+    }
+  }
   const float* from = held ? s_score : score;
   __syncthreads();
   uint32_t prefix = 0;
@@ -283,35 +292,42 @@ static __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(cons
   }
 }
 
-// One warp per (KV head, sequence, K or V, 128-byte strip of a row): the kept rows' strips move down
-// in place through a ring of kDepth chunks of 32 rows in shared memory.  Row j comes from slot
-// keep[j] >= j: a chunk is written once it and all before it were read, and rows that were written
-// are never read again, so reading ahead needs nothing but that order, and no warp waits for
-// another.  Bound by the bytes: each kept row is read and written once, by whole lines of L2.
-template <int kDepth>
-__global__ void __launch_bounds__(32) evict_move_kernel(const __grid_constant__ EvictArgs a, int eb) {
+// One block per (KV head, sequence, K or V, 128-byte strip of a row): the kept rows' strips move
+// down in place, chunks of 32 rows dealt to the warps in turn, each with a ring of kMoveDepth of them
+// in shared memory.  Row j comes from slot keep[j] >= j: a round's chunks are written once they and
+// all before them were read, and rows that were written are never read again, so reading ahead needs
+// nothing but that order.  Bound by the bytes: each kept row is read and written once, by whole lines
+// of L2.  Eight warps: one alone moves about 8 GB/s, so few strips need many, and for many strips
+// the barrier of a round costs little (8 heads of 128 bf16 dims, 1 / 2 / 4 / 8 / 16 warps: 30000
+// keys of one sequence cut to 20000 388 / 229 / 142 / 116 / 108 us, 32 sequences of 4000 cut to
+// 2000 87 / 87 / 81 / 76 / 82 us).
+constexpr int kMoveWarps = 8, kMoveDepth = 3;
+constexpr int kMoveRing = kMoveDepth * (4096 + 256);       // bytes of a warp: rows and where they go
+static __global__ void __launch_bounds__(kMoveWarps * 32) evict_move_kernel(const __grid_constant__ EvictArgs a,
+                                                                            int eb) {
   extern __shared__ __align__(128) char smem[];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x, part = blockIdx.x, g = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = blockIdx.x, g = blockIdx.y;
   const int64_t seq = blockIdx.z, sg = seq * a.c.n_kv + g;
-  if (part == 0 && g == 0 && lane == 0) a.new_lens[seq] = a.new_ws[seq];
+  if (part == 0 && g == 0 && threadIdx.x == 0) a.new_lens[seq] = a.new_ws[seq];
   if (!a.cut[sg]) return;
   const int32_t* keep = a.keep + sg * a.budget;
   const int32_t* table = a.c.tables + seq * a.c.max_pages;
   const int col = (part >> 1) * 128 + (lane & 7) * 16, sub = lane >> 3, budget = a.budget;
   char* base = static_cast<char*>(part & 1 ? a.vp : a.kp) + g * a.c.head_stride * eb + col;
   const bool mine = col < a.c.hd * eb;
-  const uint32_t ring = sm100::smem_addr(smem) + lane * 16;
-  int64_t* s_to = reinterpret_cast<int64_t*>(smem + kDepth * 4096);    // [kDepth][32] byte offsets
-  const int chunks = (budget + 31) / 32;
+  char* own = smem + warp * kMoveRing;
+  const uint32_t ring = sm100::smem_addr(own) + lane * 16;
+  int64_t* s_to = reinterpret_cast<int64_t*>(own + kMoveDepth * 4096);    // [kMoveDepth][32] byte offsets
+  const int rounds = (budget + 32 * kMoveWarps - 1) / (32 * kMoveWarps);                // of a chunk per warp
   const uint32_t page_size = static_cast<uint32_t>(a.c.page_size);
   auto offset = [&](int slot, int32_t page) -> int64_t {
     const int in = slot - static_cast<int>(static_cast<uint32_t>(slot) / page_size * page_size);
     return (page * a.c.page_stride + in * a.c.slot_stride) * eb;
   };
   auto valid = [&](int32_t page) { return page >= 0 && page < a.c.n_pages; };
-  // The lookups of four chunks at once, two and one turns of the loop ahead of their use: a lane's
+  // The lookups of four of the warp's chunks at once, two and one turns of the loop ahead of their use: a lane's
   // slots first, then the pages of where its rows come from and go.
   struct Rows4 {
     int slot[4];
@@ -320,14 +336,14 @@ __global__ void __launch_bounds__(32) evict_move_kernel(const __grid_constant__ 
   auto load_slots = [&](int c, Rows4& x) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int j = (c + k) * 32 + lane;
+      const int j = ((c + k) * kMoveWarps + warp) * 32 + lane;
       x.slot[k] = j < budget ? keep[j] : -1;
     }
   };
   auto load_pages = [&](int c, Rows4& x) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int j = (c + k) * 32 + lane;
+      const int j = ((c + k) * kMoveWarps + warp) * 32 + lane;
       const bool moves = x.slot[k] > j;                // (a row that stays is left alone)
       x.from[k] = moves ? table[static_cast<uint32_t>(x.slot[k]) / page_size] : 0;
       x.to[k] = moves ? table[static_cast<uint32_t>(j) / page_size] : 0;
@@ -338,18 +354,18 @@ __global__ void __launch_bounds__(32) evict_move_kernel(const __grid_constant__ 
   load_pages(0, now);
   load_slots(4, next);
 #pragma unroll 1
-  for (int c = 0; c < chunks + kDepth; c += 4) {
+  for (int c = 0; c < rounds + kMoveDepth; c += 4) {
     Rows4 after;
     load_slots(c + 8, after);
     load_pages(c + 4, next);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int in = c + k, out = in - kDepth, j = in * 32 + lane;
-      const uint32_t at = ring + (in % kDepth) * 4096;
-      int64_t* to = s_to + (in % kDepth) * 32;
-      if (out >= 0 && out < chunks) {
-        copy_wait<kDepth - 1>();
-        __syncwarp();                     // all lanes' copies of this chunk have landed
+      const int in = c + k, out = in - kMoveDepth, j = (in * kMoveWarps + warp) * 32 + lane;
+      const uint32_t at = ring + (in % kMoveDepth) * 4096;
+      int64_t* to = s_to + (in % kMoveDepth) * 32;
+      if (out >= 0 && out < rounds) {
+        copy_wait<kMoveDepth - 1>();
+        __syncthreads();                  // the round's copies have landed
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int64_t row = to[4 * i + sub];
@@ -357,7 +373,7 @@ __global__ void __launch_bounds__(32) evict_move_kernel(const __grid_constant__ 
         }
         __syncwarp();
       }
-      if (in < chunks) {
+      if (in < rounds) {
         int64_t from = -1, dest = -1;
         if (now.slot[k] > j) {
           if (valid(now.from[k]) && valid(now.to[k])) {

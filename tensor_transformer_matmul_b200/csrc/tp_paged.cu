@@ -363,16 +363,9 @@ extern "C" tp_status tp_kv_evict_paged(const tp_paged_desc* desc, void* score, c
   tp::ProfScope prof(s, "kv_evict_move");
   const dim3 grid(static_cast<unsigned>(2 * a.strips), static_cast<unsigned>(desc->n_kv),
                   static_cast<unsigned>(desc->b));
-  // few warps: deep rings, so that each alone has enough in flight
-  const int64_t warps = static_cast<int64_t>(grid.x) * grid.y * grid.z;
-#define TP_MOVE(D)                                                                            \
-  do {                                                                                        \
-    TP_CUDA_TRY(cudaFuncSetAttribute(tp::paged::evict_move_kernel<D>,                         \
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, D * 4352)); \
-    TP_LAUNCH_PDL(tp::paged::evict_move_kernel<D>, grid, dim3(32), D * 4352, s, a, eb);       \
-  } while (0)
-  if (warps <= 3 * tp::num_sms()) TP_MOVE(16);
-  else TP_MOVE(6);
-#undef TP_MOVE
+  constexpr int smem = tp::paged::kMoveWarps * tp::paged::kMoveRing;
+  TP_CUDA_TRY(cudaFuncSetAttribute(tp::paged::evict_move_kernel,
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  TP_LAUNCH_PDL(tp::paged::evict_move_kernel, grid, dim3(tp::paged::kMoveWarps * 32), smem, s, a, eb);
   return TP_OK;
 }
