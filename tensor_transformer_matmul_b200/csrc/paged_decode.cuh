@@ -89,8 +89,9 @@ template <int HDP_, int NT>
 struct Mma {
   using T = __nv_bfloat16;
   static constexpr int HDP = HDP_, kHeads = 8 * NT, kStep = 16, kOwn = 2 * NT, kKeys = 2;
-  static constexpr int kRowBytes = HDP * 2;
+  static constexpr int kRowBytes = HDP * 2, kStages = 2;
   static constexpr int kShared = 0;                 // block-wide and per-warp scratch
+  static constexpr bool kRedo = false;
   static constexpr int kWarpShared = 0;
   uint32_t q[HDP / 32][NT][4];
   float acc[HDP / 16][NT][4];
@@ -213,6 +214,211 @@ struct Mma {
   }
 };
 
+// Two fp32 numbers as the sums of three bf16 numbers each (every remainder is exact; numbers that
+// round to an infinite bf16 have no parts).
+__device__ __forceinline__ void cut3(float a, float b, uint32_t (&w)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    w[i] = pack_bf16x2(a, b);
+    a -= bf16lo(w[i]);
+    b -= bf16hi(w[i]);
+  }
+}
+
+// fp32 on the same instructions: a number is the sum of three bf16 numbers, each at most 2^-9 of the
+// one before, and of the nine products of two sums the six largest are taken; what is left out is
+// below 2^-25 of the product.  The instructions' own sums are cut off, not rounded, so they run over
+// one step or 16 dims only, and fp32 additions join them.  A cut costs 5.5 instructions a number once,
+// plain fp32 products one a head.  Layout as above with four dims to
+// 16 bytes; the queries' parts lie in shared memory as the lanes' operands.
+template <int HDP_, int NT>
+struct MmaF32 {
+  using T = float;
+  static constexpr int HDP = HDP_, kHeads = 8 * NT, kStep = 16, kOwn = 2 * NT, kKeys = 2;
+  static constexpr int kRowBytes = HDP * 4, kStages = 1;
+  static constexpr int kShared = HDP / 16 * NT * 3 * 256;      // [16 dims][tile][part][lane] pairs
+  static constexpr int kWarpShared = 0;
+  static constexpr bool kRedo = true;
+  float acc[HDP / 16][NT][4];
+
+  __device__ __forceinline__ static int head(int i, int t) { return (i >> 1) * 8 + 2 * t + (i & 1); }
+  // (every warp writes the same values)
+  __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, float, char* sq, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int c0 = 0; c0 < HDP / 16; c0 += 8 / NT) {    // eight loads in flight
+      float4 x[8 / NT][NT];
+#pragma unroll
+      for (int c = 0; c < 8 / NT; ++c)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const int d = (c0 + c) * 16 + t * 4;
+          x[c][n] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c0 + c < HDP / 16 && n * 8 + g < heads && d < hd)
+            x[c][n] = *reinterpret_cast<const float4*>(qp + (n * 8 + g) * hs + d);
+        }
+#pragma unroll
+      for (int c = 0; c < 8 / NT; ++c)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if (c0 + c >= HDP / 16) continue;
+          uint32_t lo[3], hi[3];
+          cut3(x[c][n].x, x[c][n].y, lo);
+          cut3(x[c][n].z, x[c][n].w, hi);
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            *reinterpret_cast<uint2*>(sq + (((c0 + c) * NT + n) * 3 + i) * 256 + lane * 8) = make_uint2(lo[i], hi[i]);
+        }
+    }
+    __syncwarp();
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < HDP / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][n][r] = 0.f;
+  }
+  __device__ __forceinline__ void scores(uint32_t kbuf, float (&z)[kOwn][kKeys], float scale, char* sq, int lane) {
+    const int g = lane >> 2, t = lane & 3, flip = ((g >> 2) ^ g) & 1;
+    const uint32_t at = kbuf + g * kRowBytes + (t ^ (g & 2)) * 16;
+    const uint32_t even = at + flip * 64, odd = at + (flip ^ 1) * 64;
+    float s[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) s[n][r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < HDP / 16; ++c) {
+      const uint32_t k = (c & 1 ? odd : even) + (c & ~1) * 64;
+      const uint4 x = lds16(k), y = lds16(k + 8 * kRowBytes);
+      uint32_t x0[3], x1[3], y0[3], y1[3];
+      cut3(__uint_as_float(x.x), __uint_as_float(x.y), x0);
+      cut3(__uint_as_float(x.z), __uint_as_float(x.w), x1);
+      cut3(__uint_as_float(y.x), __uint_as_float(y.y), y0);
+      cut3(__uint_as_float(y.z), __uint_as_float(y.w), y1);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint2 q[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          q[i] = *reinterpret_cast<const uint2*>(sq + ((c * NT + n) * 3 + i) * 256 + lane * 8);
+        // (part of the key, part of the query), the smallest first
+        float u[4] = {0.f, 0.f, 0.f, 0.f};
+        mma16816(u, x0[2], y0[2], x1[2], y1[2], q[0].x, q[0].y);
+        mma16816(u, x0[0], y0[0], x1[0], y1[0], q[2].x, q[2].y);
+        mma16816(u, x0[1], y0[1], x1[1], y1[1], q[1].x, q[1].y);
+        mma16816(u, x0[1], y0[1], x1[1], y1[1], q[0].x, q[0].y);
+        mma16816(u, x0[0], y0[0], x1[0], y1[0], q[1].x, q[1].y);
+        mma16816(u, x0[0], y0[0], x1[0], y1[0], q[0].x, q[0].y);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[n][r] += u[r];
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) z[2 * n + i][k] = s[n][2 * k + i] * scale;
+  }
+  // An infinite number has no parts: scores that came out as NaN are taken again in plain fp32.
+  __device__ __noinline__ static void redo_scores(uint32_t kbuf, float (&z)[kOwn][kKeys], float scale,
+                                                  const T* qp, int64_t hs, int heads, int hd, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+      for (int k = 0; k < kKeys; ++k) {
+        if (head(i, t) >= heads) continue;
+        const int row = g + 8 * k;
+        float s = 0.f;
+        for (int d = 0; d < hd; d += 4) {
+          const uint4 x = lds16(kbuf + row * kRowBytes + ((d >> 2) ^ swizzle(row)) * 16);
+          const float4 y = *reinterpret_cast<const float4*>(qp + head(i, t) * hs + d);
+          s = fmaf(__uint_as_float(x.x), y.x, s);
+          s = fmaf(__uint_as_float(x.y), y.y, s);
+          s = fmaf(__uint_as_float(x.z), y.z, s);
+          s = fmaf(__uint_as_float(x.w), y.w, s);
+        }
+        z[i][k] = s * scale;
+      }
+  }
+  __device__ __forceinline__ static void keep_scores(float* to, const float (&z)[kOwn][kKeys], int k,
+                                                     int t, int room) {
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (8 * n + 2 * t < room)
+        *reinterpret_cast<float2*>(to + 8 * n + 2 * t) = make_float2(z[2 * n][k], z[2 * n + 1][k]);
+  }
+  __device__ __forceinline__ void rescale(const float (&corr)[kOwn]) {
+#pragma unroll
+    for (int i = 0; i < HDP / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][n][r] *= corr[2 * n + (r & 1)];
+  }
+  __device__ __forceinline__ void add_values(uint32_t vbuf, const float (&p)[kOwn][kKeys], char*, int lane) {
+    const int g = lane >> 2, t = lane & 3, sw = ((t & 2) << 1) | ((t & 1) << 1);
+    const uint32_t row0 = vbuf + 2 * t * kRowBytes + (g ^ sw) * 16;
+    const uint32_t row1 = vbuf + (2 * t + 1) * kRowBytes + (g ^ sw ^ 4) * 16;
+    uint32_t w[NT][2][3];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        cut3(p[2 * n][k], p[2 * n + 1][k], w[n][k]);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) w[n][k][i] = transpose8x8(w[n][k][i]);
+      }
+#pragma unroll
+    for (int v = 0; v < HDP / 32; ++v) {
+      float r[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 x = lds16((k & 1 ? row1 : row0) + (k >> 1) * 8 * kRowBytes + v * 128);
+        r[k][0] = __uint_as_float(x.x); r[k][1] = __uint_as_float(x.y);
+        r[k][2] = __uint_as_float(x.z); r[k][3] = __uint_as_float(x.w);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t a0[3], a1[3], a2[3], a3[3];
+        cut3(r[0][2 * i], r[1][2 * i], a0);
+        cut3(r[0][2 * i + 1], r[1][2 * i + 1], a1);
+        cut3(r[2][2 * i], r[3][2 * i], a2);
+        cut3(r[2][2 * i + 1], r[3][2 * i + 1], a3);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float to[4] = {0.f, 0.f, 0.f, 0.f};
+          mma16816(to, a0[2], a1[2], a2[2], a3[2], w[n][0][0], w[n][1][0]);
+          mma16816(to, a0[0], a1[0], a2[0], a3[0], w[n][0][2], w[n][1][2]);
+          mma16816(to, a0[1], a1[1], a2[1], a3[1], w[n][0][1], w[n][1][1]);
+          mma16816(to, a0[1], a1[1], a2[1], a3[1], w[n][0][0], w[n][1][0]);
+          mma16816(to, a0[0], a1[0], a2[0], a3[0], w[n][0][1], w[n][1][1]);
+          mma16816(to, a0[0], a1[0], a2[0], a3[0], w[n][0][0], w[n][1][0]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[2 * v + i][n][r] += to[r];
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void store(float* out, int lane) const {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int i = 0; i < HDP / 16; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int d = (i >> 1) * 32 + g * 4 + 2 * (i & 1);
+          *reinterpret_cast<float2*>(out + (n * 8 + 2 * t + h) * HDP + d) =
+              make_float2(acc[i][n][h], acc[i][n][2 + h]);
+        }
+  }
+};
+
 // fp32: G heads (1, 4 or 8); a step is 8 keys.  Four lanes share a key's dims and then its heads:
 // a lane's scores: key g, heads HPL t and the next (G == 1: all four the same).  A lane owns four
 // dims of the output (HDP 256: eight; HDP 64: of every other key).
@@ -220,8 +426,9 @@ template <int HDP_, int G>
 struct Simt {
   using T = float;
   static constexpr int HDP = HDP_, kHeads = G, kStep = 8, kOwn = G >= 4 ? G / 4 : 1, kKeys = 1;
-  static constexpr int kRowBytes = HDP * 4;
+  static constexpr int kRowBytes = HDP * 4, kStages = 2;
   static constexpr int kShared = G * HDP * 4;
+  static constexpr bool kRedo = false;
   static constexpr int kWarpShared = 8 * G * 4;
   static constexpr int kLanes = HDP / 4 < 32 ? HDP / 4 : 32;   // lanes of a row of V
   static constexpr int kRows = 32 / kLanes;                    // rows of a copy of V
@@ -345,12 +552,22 @@ struct Simt {
   }
 };
 
-// shared memory of a warp's ring: two steps of keys and values
+// shared memory of a warp's ring: two steps of keys and values, or one (kStages) where a step computes
+// long enough for twice the warps to keep the memory busy
 template <typename E>
-constexpr int ring_bytes() { return 4 * E::kStep * E::kRowBytes; }
-template <typename E, int W>
-constexpr int decode_smem() {
-  return W * (ring_bytes<E>() + E::kWarpShared) + E::kShared + W * E::kHeads * 8;
+constexpr int ring_bytes() { return 2 * E::kStages * E::kStep * E::kRowBytes; }
+// Warps of a block that has a row to itself (192 KB of rings, the SM's whole), warps of a block of a
+// split launch, and how many of these share an SM.
+constexpr int kRings = 192 * 1024;
+constexpr int whole_warps(int ring) { return ring * 12 <= kRings ? 12 : kRings / ring; }
+constexpr int whole_blocks(int rings) { return rings * 2 <= kRings ? 2 : 1; }   // at least, on an SM
+constexpr int split_warps(int ring) { return ring * 6 <= kRings ? 6 : kRings / ring; }
+constexpr int split_blocks(int ring) {
+  return kRings / (split_warps(ring) * ring) < 3 ? kRings / (split_warps(ring) * ring) : 3;
+}
+template <typename E>
+constexpr int decode_smem(int warps) {
+  return warps * (ring_bytes<E>() + E::kWarpShared) + E::kShared + warps * E::kHeads * 8;
 }
 
 // Keys k0 .. k1-1 of (sequence, KV head g), heads j0 .. j0+heads-1: this warp's share of them.
@@ -394,21 +611,21 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
   // address of the pool, and nothing is read), so are the dims that pad a row.
   // Eight lanes copy 128 consecutive bytes of a row, so that every request is a whole line of L2
   // (with 32 and 64 bytes of a row to a request the kernel stopped at 4.6 TB/s).
-  auto issue = [&](int64_t row, uint32_t mask, int s) {
+  // Keys (kv 0), values (kv 1) or both, each a group.
+  auto issue = [&](int64_t row, uint32_t mask, int s, int first, int last) {
     constexpr int kPtrs = E::kStep / 4, kLines = E::kRowBytes / 128;
     const int j = lane >> 3;
-    const uint32_t to = buf + (s & 1) * 2 * kBuf + j * E::kRowBytes;
+    const uint32_t to = buf + (s % E::kStages) * 2 * kBuf + j * E::kRowBytes;
     const uint32_t to0 = to + ((lane & 7) ^ swizzle(j)) * 16, to1 = to + ((lane & 7) ^ swizzle(j + 4)) * 16;
     int64_t off[kPtrs];
     bool in[kPtrs];
-    __syncwarp();                                 // every lane has read what was there
 #pragma unroll
     for (int i = 0; i < kPtrs; ++i) {
       off[i] = __shfl_sync(0xffffffffu, row, s * E::kStep + 4 * i + j);
       in[i] = (mask >> (s * E::kStep + 4 * i + j)) & 1u;
     }
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
+    for (int kv = first; kv <= last; ++kv) {
 #pragma unroll
       for (int i = 0; i < kPtrs; ++i)
 #pragma unroll
@@ -427,31 +644,62 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
 
   int chunk = k0 / kChunk + warp;
   const int end = (k1 + kChunk - 1) / kChunk;
+  const T* qp = static_cast<const T*>(a.q.p) + seq * a.q.ts + j0 * a.q.hs;
+  if constexpr (E::kShared == 0) e.load_q(qp, a.q.hs, heads, hd, a.scale, bsh, lane);
   int64_t row = 0;
   uint32_t mask = 0;
   Entry entry{-1, 0};
   if (chunk < end) {
     const int key = chunk * kChunk + lane;
     row = row_of(key, entry_of(key), mask);
-    issue(row, mask, 0);
-    issue(row, mask, 1);
+#pragma unroll
+    for (int s = 0; s < E::kStages; ++s) issue(row, mask, s, 0, 1);
     if (chunk + W < end) entry = entry_of(key + W * kChunk);
   }
+  // queries that go to shared memory: while the first rows are on their way
+  if constexpr (E::kShared > 0) e.load_q(qp, a.q.hs, heads, hd, a.scale, bsh, lane);
   for (; chunk < end; chunk += W) {
     const bool more = chunk + W < end;
     int64_t row_n = 0;
     uint32_t mask_n = 0;
+    // what follows in the freed buffers: keys, values or both of the step kStages later
+    auto issue_next = [&](int s, int first, int last) {
+      const int ahead = s + E::kStages;
+      __syncwarp();                               // every lane has read what was there
+      if (ahead < NS) {
+        issue(row, mask, ahead, first, last);
+      } else if (more) {
+        if (ahead == NS && first == 0) {
+          const int key = (chunk + W) * kChunk + lane;
+          row_n = row_of(key, entry, mask_n);
+          if (chunk + 2 * W < end) entry = entry_of(key + W * kChunk);
+        }
+        issue(row_n, mask_n, ahead - NS, first, last);
+      } else {
+        for (int kv = first; kv <= last; ++kv) copy_commit();
+      }
+    };
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      const uint32_t kb = buf + (s & 1) * 2 * kBuf;
+      const uint32_t kb = buf + (s % E::kStages) * 2 * kBuf;
+      constexpr int kPending = 2 * E::kStages - 1;   // groups in flight behind the one waited for
       constexpr uint32_t kAll = (1u << E::kStep) - 1u;
       const uint32_t live = (mask >> (s * E::kStep)) & kAll;
-      copy_wait<3>();                             // this step's keys are there
+      copy_wait<kPending>();                      // this step's keys are there
       __syncwarp();
       if (live) {
         seen = true;
         float z[E::kOwn][E::kKeys];
         e.scores(kb, z, a.scale, bsh, lane);
+        if constexpr (E::kRedo) {
+          bool nan = false;
+#pragma unroll
+          for (int i = 0; i < E::kOwn; ++i)
+#pragma unroll
+            for (int k = 0; k < E::kKeys; ++k) nan |= z[i][k] != z[i][k];
+          if (__any_sync(0xffffffffu, nan))
+            E::redo_scores(kb, z, a.scale, qp, a.q.hs, heads, hd, lane);
+        }
         if (a.z != nullptr) {
 #pragma unroll
           for (int k = 0; k < E::kKeys; ++k)
@@ -496,26 +744,22 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
             z[i][k] = exp2_f(z[i][k] - base_of(m[i]));
             l[i] += z[i][k];
           }
-        copy_wait<2>();                           // and its values
+        if constexpr (E::kStages == 1) issue_next(s, 0, 0);
+        copy_wait<2 * E::kStages - 2 + (E::kStages == 1)>();   // and its values
         __syncwarp();
         e.add_values(kb + kBuf, z, wsh, lane);
       }
-      copy_wait<2>();                             // (nothing lands in the slot any more)
+      if constexpr (E::kStages == 1) {
+        if (!live) issue_next(s, 0, 0);
+        copy_wait<1>();                           // (nothing lands in the values' buffer any more)
+        issue_next(s, 1, 1);
+      } else {
+        copy_wait<2>();
+        issue_next(s, 0, 1);
+      }
       if (a.z != nullptr && live != kAll && lane < E::kStep && !((live >> lane) & 1u)) {
         const int key = chunk * kChunk + s * E::kStep + lane;
         if (key < k1) *z_row(key) = __uint_as_float(kLeftOut);
-      }
-      // the ring's slot is free: the step after the next
-      if (s + 2 < NS) {
-        issue(row, mask, s + 2);
-      } else {
-        if (s + 2 == NS && more) {
-          const int key = (chunk + W) * kChunk + lane;
-          row_n = row_of(key, entry, mask_n);
-          if (chunk + 2 * W < end) entry = entry_of(key + W * kChunk);
-        }
-        if (more) issue(row_n, mask_n, s + 2 - NS);
-        else copy_commit(), copy_commit();
       }
     }
     row = row_n;
@@ -611,7 +855,6 @@ __device__ __forceinline__ void block_piece(const DecodeArgs& a, E& e, int64_t s
   const int hd = a.c.hd;
   const int busy = min(W, (k1 - k0 + kChunk - 1) / kChunk);     // warps that get keys
   if (warp < busy) {
-    e.load_q(static_cast<const T*>(a.q.p) + seq * a.q.ts + j0 * a.q.hs, a.q.hs, heads, hd, a.scale, bsh, lane);
     warp_pass<E, W>(a, e, seq, g, j0, heads, k0, k1, ring, wsh, bsh, sm + warp * E::kHeads,
                     sl + warp * E::kHeads, warp, lane);
   }
@@ -653,12 +896,9 @@ __device__ __forceinline__ void block_piece(const DecodeArgs& a, E& e, int64_t s
   __syncthreads();
 }
 
-// Blocks of a split launch that share an SM (by their rings), and the registers that leaves them.
-constexpr int split_blocks(int hdp) { return hdp == 64 ? 3 : hdp == 128 ? 2 : 1; }
-
 // One block per (head tile, KV head, sequence).
 template <typename E, int W>
-__global__ void __launch_bounds__(W * 32) decode_whole_kernel(const __grid_constant__ DecodeArgs a) {
+__global__ void __launch_bounds__(W * 32, whole_blocks(W * ring_bytes<E>())) decode_whole_kernel(const __grid_constant__ DecodeArgs a) {
   extern __shared__ __align__(128) char smem[];
   pdl_wait();
   pdl_trigger();
@@ -672,9 +912,9 @@ __global__ void __launch_bounds__(W * 32) decode_whole_kernel(const __grid_const
   if (a.z != nullptr && a.tiles == 1) {
     const float* lse = a.lse + seq * a.c.n_q + g * a.c.group;
     float* s_lse = reinterpret_cast<float*>(smem);
-    if (threadIdx.x < a.c.group) s_lse[threadIdx.x] = lse[threadIdx.x] * kLog2e;
+    for (int h = threadIdx.x; h < a.c.group; h += blockDim.x) s_lse[h] = lse[h] * kLog2e;
     __syncthreads();
-    add_weights(a, seq, g, n, s_lse, lse, threadIdx.x, W * 32);
+    add_weights(a, seq, g, n, s_lse, lse, threadIdx.x, blockDim.x);
   }
 }
 
@@ -691,8 +931,10 @@ __device__ __forceinline__ int64_t units_per_run(const DecodeArgs& a, int64_t un
 }
 
 // One block per run of units.
-template <typename E, int W>
-__global__ void __launch_bounds__(W * 32, split_blocks(E::HDP)) decode_split_kernel(const __grid_constant__ DecodeArgs a) {
+template <typename E>
+__global__ void __launch_bounds__(split_warps(ring_bytes<E>()) * 32, split_blocks(ring_bytes<E>()))
+    decode_split_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int W = split_warps(ring_bytes<E>());
   extern __shared__ __align__(128) char smem[];
   __shared__ int64_t s_sum[W], s_seq, s_first;
   pdl_wait();

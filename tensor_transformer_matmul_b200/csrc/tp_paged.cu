@@ -34,6 +34,9 @@ tp_status check_vec_rows(const tp_head_rows* r, int64_t T, int heads, int hd, in
 tp::rope::Rows rows_of(const tp_head_rows* r) { return {r->data, r->token_stride, r->head_stride}; }
 
 // ---- decode attention: which kernel, and its workspace ----
+// fp32 groups of up to this many heads multiply on the SIMT units
+constexpr int kSimtHeads = 1;
+
 // heads of a tile and blocks of a split launch per SM: of the padded head size and the group
 struct DecodePlan {
   int hdp, heads, tiles, runs;
@@ -44,7 +47,7 @@ DecodePlan decode_plan(const tp::paged::View& c, int dtype) {
   DecodePlan p;
   p.hdp = c.hd <= 64 ? 64 : c.hd <= 128 ? 128 : 256;
   if (dtype == TP_BF16) p.heads = c.group > 8 && p.hdp < 256 ? 16 : 8;
-  else p.heads = c.group == 1 ? 1 : c.group <= 4 ? 4 : 8;
+  else p.heads = c.group <= kSimtHeads ? c.group : c.group > 8 && p.hdp < 256 ? 16 : 8;
   p.tiles = static_cast<int>(tp::ceil_div(c.group, p.heads));
   // One block per (sequence, KV head, head tile) or runs of equal length?  A block alone streams
   // about 0.1 TB/s; a split launch costs about 7 us more (the cuts' joins, a second kernel) but no
@@ -54,9 +57,11 @@ DecodePlan decode_plan(const tp::paged::View& c, int dtype) {
   // split: 1 x 700 keys 7.3 / 10.2 us, 1 x 4000 24.8 / 14.2, 16 ragged up to 1500 14.8 / 21.8,
   // 16 up to 4096 29.6 / 35.2, 64 up to 700 26 / 40, 16 up to 8000 56 / 58.
   const int64_t blocks = c.b * c.n_kv * p.tiles;
-  const int64_t row = c.cap * c.hd * 2 * tp::elem_bytes(dtype);
+  // (fp32 groups compute about four times as long per byte: 3 x 1123 keys of 64 / 8 fp32 heads of 128
+  // dims 23.5 us whole.)
+  const int64_t row = c.cap * c.hd * 2 * tp::elem_bytes(dtype) * (dtype == TP_F32 && p.heads > kSimtHeads ? 4 : 1);
   p.whole = row <= (3 << 18) || (row <= (5 << 19) && blocks * 3 >= tp::num_sms());
-  p.runs = tp::num_sms() * tp::paged::split_blocks(p.hdp);
+  p.runs = tp::num_sms() * tp::paged::split_blocks(128 * p.hdp);   // (all engines' rings)
   return p;
 }
 
@@ -82,21 +87,32 @@ DecodeWs decode_ws(const tp::paged::View& c, int dtype, bool with_score) {
   return w;
 }
 
+template <typename E, int W>
+tp_status launch_whole(const tp::paged::DecodeArgs& a, dim3 grid, cudaStream_t s) {
+  constexpr int smem = tp::paged::decode_smem<E>(W);
+  auto* whole = tp::paged::decode_whole_kernel<E, W>;
+  TP_CUDA_TRY(cudaFuncSetAttribute(whole, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  TP_LAUNCH_PDL(whole, grid, dim3(W * 32), smem, s, a);
+  return TP_OK;
+}
+
 template <typename E>
 tp_status launch_decode(const tp::paged::DecodeArgs& a, const DecodePlan& p, cudaStream_t s) {
   using namespace tp::paged;
-  constexpr int kWhole = E::HDP == 256 ? 6 : 12, kSplit = 6;
-  const int smem = p.whole ? decode_smem<E, kWhole>() : decode_smem<E, kSplit>();
-  auto* whole = decode_whole_kernel<E, kWhole>;
-  auto* split = decode_split_kernel<E, kSplit>;
-  auto* kern = p.whole ? whole : split;
-  TP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  static_assert(ring_bytes<E>() == 128 * E::HDP, "decode_plan's");
+  constexpr int kWhole = whole_warps(ring_bytes<E>()), kSplit = split_warps(ring_bytes<E>());
   tp::ProfScope prof(s, "attn_decode_paged");
   if (p.whole) {
-    TP_LAUNCH_PDL(whole, dim3(static_cast<unsigned>(a.c.n_kv * a.tiles), static_cast<unsigned>(a.c.b)),
-                  dim3(kWhole * 32), smem, s, a);
-    return TP_OK;
+    // no more warps than the row's room has units, so that blocks of short rows share an SM
+    const int64_t units = tp::ceil_div(a.c.cap, kChunk);
+    const dim3 grid(static_cast<unsigned>(a.c.n_kv * a.tiles), static_cast<unsigned>(a.c.b));
+    if (units <= 4) return launch_whole<E, 4>(a, grid, s);
+    if (units <= 8 && kWhole > 8) return launch_whole<E, 8 < kWhole ? 8 : kWhole>(a, grid, s);
+    return launch_whole<E, kWhole>(a, grid, s);
   }
+  constexpr int smem = decode_smem<E>(kSplit);
+  auto* split = decode_split_kernel<E>;
+  TP_CUDA_TRY(cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   TP_LAUNCH_PDL(split, dim3(static_cast<unsigned>(a.runs)), dim3(kSplit * 32), smem, s, a);
   auto* join = join_kernel<typename E::T, E::kHeads>;
   TP_LAUNCH_PDL(join, dim3(static_cast<unsigned>(a.c.n_q), static_cast<unsigned>(a.c.b)), dim3(128), 0, s, a);
@@ -281,14 +297,15 @@ extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_he
   a.min_units = 4;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   using tp::paged::Mma;
+  using tp::paged::MmaF32;
   using tp::paged::Simt;
 #define TP_DECODE(H)                                                                             \
   (desc->dtype == TP_BF16                                                                        \
        ? (p.heads == 8 ? launch_decode<Mma<H, 1>>(a, p, s)                                       \
                        : launch_decode<Mma<H, H == 256 ? 1 : 2>>(a, p, s))                       \
        : (p.heads == 1 ? launch_decode<Simt<H, 1>>(a, p, s)                                      \
-                       : p.heads == 4 ? launch_decode<Simt<H, 4>>(a, p, s)                       \
-                                      : launch_decode<Simt<H, 8>>(a, p, s)))
+                       : p.heads == 8 ? launch_decode<MmaF32<H, 1>>(a, p, s)                     \
+                                      : launch_decode<MmaF32<H, H == 256 ? 1 : 2>>(a, p, s)))
   st = p.hdp == 64 ? TP_DECODE(64) : p.hdp == 128 ? TP_DECODE(128) : TP_DECODE(256);
 #undef TP_DECODE
   if (st != TP_OK || !score || (p.whole && p.tiles == 1)) return st;

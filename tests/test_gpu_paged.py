@@ -128,6 +128,10 @@ DECODE = [
     ([50, 129], 66, 2, 96, 3, "f32"),
     ([130, 2], 66, 2, 72, 32, "bf16"),
     ([128, 129], 3, 3, 8, 128, "bf16"),
+    ([40, 3], 70, 1, 16, 8, "bf16"),
+    ([40, 700, 1, 90], 8, 2, 40, 16, "f32"),
+    ([40, 2100, 1, 90], 8, 1, 256, 16, "f32"),
+    ([40, 2100, 1, 90], 32, 2, 128, 16, "f32"),
     ([40, 700, 1, 90], 4, 4, 32, 16, "bf16"),
     ([2049, 512, 513, 90, 1025], 16, 2, 128, 32, "bf16"),
     ([2049, 512, 513, 90, 1025], 4, 2, 128, 32, "f32"),
@@ -185,9 +189,10 @@ def test_decode_extreme_values(lib):
     c.check(*c.decode(), before)
 
 
-def test_decode_infinite_keys(lib):
+@pytest.mark.parametrize("n_q,dtype", [(4, "bf16"), (4, "f32"), (1, "f32"), (16, "f32")])
+def test_decode_infinite_keys(lib, n_q, dtype):
     # a key with a score of -infinity has weight 0; all of them: no softmax (NaN), lse -infinity
-    c = Cache(lib, [100, 40], 4, 1, 64, 16)
+    c = Cache(lib, [100, 40], n_q, 1, 64, 16, dtype)
     c.q[..., 0] = 1.0
     kp, vp, tables = c.host()
     hit = [s for s in range(100) if s % 3 == 0 or s < 40]
@@ -198,18 +203,18 @@ def test_decode_infinite_keys(lib):
     assert torch.isnan(o[1]).all() and torch.isneginf(lse[1]).all()
     assert torch.isnan(c.score[1, 0, :40]).all()
     kp, vp, tables = c.host()
-    for j in range(4):
+    for j in range(n_q):
         z = np.array([kp[tables[0][s // 16], 0, s % 16] @ f64(c.q)[0, j] / 8.0 for s in range(100)])
         e = np.exp(z - z.max())
         want = (e / e.sum()) @ np.stack([vp[tables[0][s // 16], 0, s % 16] for s in range(100)])
         assert np.allclose(f64(o)[0, j], want, rtol=2e-2, atol=2e-2)
     assert torch.equal(c.score[0, 0, hit], before[0, 0, hit])
     # NaN in a key: its sequence and KV head give NaN, others do not
-    c2 = Cache(lib, [100, 40], 4, 2, 64, 16)
+    c2 = Cache(lib, [100, 40], 2 * n_q, 2, 64, 16, dtype)
     c2.kp[int(c2.tables[0, 0]), 1, 3, 5] = float("nan")
     o, lse = c2.decode(with_score=False)
-    assert torch.isnan(o[0, 2:]).all() and torch.isnan(lse[0, 2:]).all()
-    assert torch.isfinite(o[0, :2].float()).all() and torch.isfinite(o[1].float()).all()
+    assert torch.isnan(o[0, n_q:]).all() and torch.isnan(lse[0, n_q:]).all()
+    assert torch.isfinite(o[0, :n_q].float()).all() and torch.isfinite(o[1].float()).all()
 
 
 def test_decode_indices_out_of_range(lib):
