@@ -1,8 +1,8 @@
 // Attention of one new token per sequence over a paged key/value cache.
 //
-// Mathematics: one pass over a sequence's keys with the running maximum m and sum l of its softmax
-// (in base 2, scores times log2 e): o = sum_n 2^(z_n - m) v_n / l.  Parts of a sequence are joined
-// by (m, l, o): each part's weight is 2^(m_part - m).  m, l, scores and o are fp32 throughout.
+// Mathematics: one pass over a sequence's keys with the running maximum m and sum l of its softmax:
+// o = sum_n e^(z_n - m) v_n / l.  Parts of a sequence are joined by (m, l, o): each part's weight is
+// e^(m_part - m).  m, l, scores and o are fp32 throughout.
 //
 // What bounds it: every key and value is read once and used by the query heads of its group, a few
 // operations per byte, so the cache's bytes do.  The kernel is built around keeping loads in flight:
@@ -32,7 +32,6 @@ namespace tp {
 namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kChunk = 32;       // keys of a unit
 
 struct DecodeArgs {
@@ -40,15 +39,15 @@ struct DecodeArgs {
   rope::Rows q, o;
   const void *kp, *vp;
   const int32_t* lens;
-  float scale;                   // times log2 e
+  float scale;
   float* lse;
   float* score;
   // split runs
   int64_t* first;                // [b + 2]: units before a sequence, of one head tile; units of a run
-  float* pm;                     // [2 * runs][heads of a tile]: maximum (base 2)
+  float* pm;                     // [2 * runs][heads of a tile]: maximum
   float* pl;                     // ... sum
   float* po;                     // ... [hd]: output before the division
-  float* z;                      // [b][n_kv][cap][zw]: base-2 scores, for the weights (may be null)
+  float* z;                      // [b][n_kv][cap][zw]: scores, for the weights (may be null)
   int64_t min_units;
   int runs, tiles, zw;           // blocks; head tiles of a group; columns of z
 };
@@ -68,11 +67,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 constexpr uint32_t kLeftOut = 0x7fc0dead;   // in place of a score: a NaN that no operation returns
-constexpr float kSlack = 8.f;
-// 2^x by the hardware's instruction (relative error 2^-22; results below 2^-126 are zeros)
-__device__ __forceinline__ float exp2_f(float x) {
+constexpr float kSlack = 5.5f;
+// e^(x - m): by the hardware's 2^x (relative error 2^-22; results below 2^-126 are zeros) of the
+// difference, which is rounded once where scores in base 2 would be rounded at their full size
+__device__ __forceinline__ float exp_above(float x, float m) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - m) * kLog2e));
   return y;
 }
 // maximum that scores are taken relative to: an all -infinity maximum gives weights of 0, not NaN
@@ -97,7 +97,7 @@ struct Mma {
   float acc[HDP / 16][NT][4];
 
   __device__ __forceinline__ static int head(int i, int t) { return (i >> 1) * 8 + 2 * t + (i & 1); }
-  __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, float, char*, int lane) {
+  __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, char*, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int c = 0; c < HDP / 32; ++c)
@@ -243,7 +243,7 @@ struct MmaF32 {
 
   __device__ __forceinline__ static int head(int i, int t) { return (i >> 1) * 8 + 2 * t + (i & 1); }
   // (every warp writes the same values)
-  __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, float, char* sq, int lane) {
+  __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, char* sq, int lane) {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int c0 = 0; c0 < HDP / 16; c0 += 8 / NT) {    // eight loads in flight
@@ -436,13 +436,12 @@ struct Simt {
   float acc[G][kCols][4];
 
   __device__ __forceinline__ static int head(int i, int t) { return G >= 4 ? t * kOwn + i : 0; }
-  // the block's queries, scaled, in shared memory (every warp writes the same values)
-  __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, float scale,
-                                         char* sq, int lane) {
+  // the block's queries in shared memory (every warp writes the same values)
+  __device__ __forceinline__ void load_q(const T* qp, int64_t hs, int heads, int hd, char* sq, int lane) {
     float* s = reinterpret_cast<float*>(sq);
     for (int i = lane; i < G * HDP; i += 32) {
       const int h = i / HDP, d = i % HDP;
-      s[i] = h < heads && d < hd ? qp[h * hs + d] * scale : 0.f;
+      s[i] = h < heads && d < hd ? qp[h * hs + d] : 0.f;
     }
     __syncwarp();
   }
@@ -454,7 +453,7 @@ struct Simt {
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[h][c][r] = 0.f;
   }
-  __device__ __forceinline__ void scores(uint32_t kbuf, float (&z)[kOwn][kKeys], float, char* sq, int lane) {
+  __device__ __forceinline__ void scores(uint32_t kbuf, float (&z)[kOwn][kKeys], float scale, char* sq, int lane) {
     const int g = lane >> 2, t = lane & 3, flip = ((g >> 2) ^ g) & 1;
     const uint32_t at = kbuf + g * kRowBytes + (t ^ (g & 2)) * 16;
     const uint32_t even = at + flip * 64, odd = at + (flip ^ 1) * 64;
@@ -477,7 +476,7 @@ struct Simt {
     if constexpr (G == 1) {
       s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
       s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
-      z[0][0] = s[0];
+      z[0][0] = s[0] * scale;
     } else {
       // halves of the heads change hands: after two exchanges a lane has the sums of its own
       float u[G / 2];
@@ -489,7 +488,7 @@ struct Simt {
 #pragma unroll
       for (int h = 0; h < G / 4; ++h) {
         const float give = t & 1 ? u[h] : u[h + G / 4], have = t & 1 ? u[h + G / 4] : u[h];
-        z[h][0] = have + __shfl_xor_sync(0xffffffffu, give, 1);
+        z[h][0] = (have + __shfl_xor_sync(0xffffffffu, give, 1)) * scale;
       }
     }
   }
@@ -645,7 +644,7 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
   int chunk = k0 / kChunk + warp;
   const int end = (k1 + kChunk - 1) / kChunk;
   const T* qp = static_cast<const T*>(a.q.p) + seq * a.q.ts + j0 * a.q.hs;
-  if constexpr (E::kShared == 0) e.load_q(qp, a.q.hs, heads, hd, a.scale, bsh, lane);
+  if constexpr (E::kShared == 0) e.load_q(qp, a.q.hs, heads, hd, bsh, lane);
   int64_t row = 0;
   uint32_t mask = 0;
   Entry entry{-1, 0};
@@ -657,7 +656,7 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
     if (chunk + W < end) entry = entry_of(key + W * kChunk);
   }
   // queries that go to shared memory: while the first rows are on their way
-  if constexpr (E::kShared > 0) e.load_q(qp, a.q.hs, heads, hd, a.scale, bsh, lane);
+  if constexpr (E::kShared > 0) e.load_q(qp, a.q.hs, heads, hd, bsh, lane);
   for (; chunk < end; chunk += W) {
     const bool more = chunk + W < end;
     int64_t row_n = 0;
@@ -714,7 +713,7 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
             }
         }
         // The scores are taken relative to a maximum that grows only where one exceeds it by more
-        // than 2^kSlack: weights up to 2^kSlack lose nothing in fp32, and most steps need no
+        // than kSlack: weights up to e^kSlack lose nothing in fp32, and most steps need no
         // exchange between lanes and no rescaling.
         bool grew = false;
 #pragma unroll
@@ -731,7 +730,7 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
             const float mn = fmaxf(m[i], x);
-            corr[i] = exp2_f(m[i] - base_of(mn));
+            corr[i] = exp_above(m[i], base_of(mn));
             m[i] = mn;
             l[i] *= corr[i];
           }
@@ -741,7 +740,7 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
         for (int i = 0; i < E::kOwn; ++i)
 #pragma unroll
           for (int k = 0; k < E::kKeys; ++k) {
-            z[i][k] = exp2_f(z[i][k] - base_of(m[i]));
+            z[i][k] = exp_above(z[i][k], base_of(m[i]));
             l[i] += z[i][k];
           }
         if constexpr (E::kStages == 1) issue_next(s, 0, 0);
@@ -783,7 +782,7 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
 
 // Weight of a part with maximum pm and sum pl where the joined maximum is m.
 __device__ __forceinline__ float part_weight(float pm, float pl, float m) {
-  return pl == 0.f || pl == -1.f ? 0.f : exp2_f(pm - base_of(m));
+  return pl == 0.f || pl == -1.f ? 0.f : exp_above(pm, base_of(m));
 }
 
 template <typename T>
@@ -799,8 +798,8 @@ __device__ __forceinline__ float inverse_sum(float l, bool none) {
   return l == 0.f ? (none ? NAN : 0.f) : 1.f / l;
 }
 
-// The weights that the group's heads gave to keys first, first + stride, ...: 2^(z - lse), heads in
-// order.  s_lse: base-2 values of the first kWeightHeads heads (lse has all, natural).
+// The weights that the group's heads gave to keys first, first + stride, ...: e^(z - lse), heads in
+// order.  s_lse: those of the first kWeightHeads heads (lse has all).
 constexpr int kWeightHeads = 64;
 __device__ __forceinline__ void add_weights(const DecodeArgs& a, int64_t seq, int g, int n,
                                             const float* s_lse, const float* lse, int first, int stride) {
@@ -830,7 +829,7 @@ __device__ __forceinline__ void add_weights(const DecodeArgs& a, int64_t seq, in
 #pragma unroll
         for (int r = 0; r < 4; ++r)
           if (h + r < a.c.group)
-            w[k] += exp2_f(v[r] - (h + r < kWeightHeads ? s_lse[h + r] : lse[h + r] * kLog2e));
+            w[k] += exp_above(v[r], h + r < kWeightHeads ? s_lse[h + r] : lse[h + r]);
       }
     }
 #pragma unroll
@@ -884,7 +883,7 @@ __device__ __forceinline__ void block_piece(const DecodeArgs& a, E& e, int64_t s
       const float inv = inverse_sum(l, none);
       T* o = static_cast<T*>(const_cast<void*>(a.o.p)) + seq * a.o.ts + (j0 + h) * a.o.hs + d;
       store4(o, s.x * inv, s.y * inv, s.z * inv, s.w * inv);
-      if (d == 0) a.lse[seq * a.c.n_q + j0 + h] = fmaf(mx, kLn2, logf(l));
+      if (d == 0) a.lse[seq * a.c.n_q + j0 + h] = mx + logf(l);
     } else {
       *reinterpret_cast<float4*>(a.po + (slot * E::kHeads + h) * hd + d) = s;
       if (d == 0) {
@@ -912,7 +911,7 @@ __global__ void __launch_bounds__(W * 32, whole_blocks(W * ring_bytes<E>())) dec
   if (a.z != nullptr && a.tiles == 1) {
     const float* lse = a.lse + seq * a.c.n_q + g * a.c.group;
     float* s_lse = reinterpret_cast<float*>(smem);
-    for (int h = threadIdx.x; h < a.c.group; h += blockDim.x) s_lse[h] = lse[h] * kLog2e;
+    for (int h = threadIdx.x; h < a.c.group; h += blockDim.x) s_lse[h] = lse[h];
     __syncthreads();
     add_weights(a, seq, g, n, s_lse, lse, threadIdx.x, blockDim.x);
   }
@@ -1047,7 +1046,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
     float mn = fmaxf(mx, pm);
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, i));
-    const float keep = exp2_f(mx - base_of(mn)), w = part_weight(pm, pl, mn);
+    const float keep = exp_above(mx, base_of(mn)), w = part_weight(pm, pl, mn);
     mx = mn;
     none |= pl == -1.f;
     l = l * keep + (pl == 0.f || pl == -1.f ? 0.f : pl * w);
@@ -1083,7 +1082,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Decod
     }
     store4(o + tid * 4, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
   }
-  if (tid == 0) a.lse[seq * a.c.n_q + j] = fmaf(mx, kLn2, logf(l));
+  if (tid == 0) a.lse[seq * a.c.n_q + j] = mx + logf(l);
 }
 
 // score += the group's weights of each key, for the cut rows and the tiled groups.
@@ -1095,7 +1094,7 @@ static __global__ void __launch_bounds__(256) weights_kernel(const __grid_consta
   const int64_t seq = blockIdx.z;
   const int n = static_cast<int>(a.c.keys(a.lens, seq));
   const float* lse = a.lse + seq * a.c.n_q + g * a.c.group;
-  for (int h = threadIdx.x; h < min(a.c.group, kWeightHeads); h += 256) s_lse[h] = lse[h] * kLog2e;
+  for (int h = threadIdx.x; h < min(a.c.group, kWeightHeads); h += 256) s_lse[h] = lse[h];
   __syncthreads();
   add_weights(a, seq, g, n, s_lse, lse, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256);
 }

@@ -281,7 +281,7 @@ extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_he
   a.kp = k_pages;
   a.vp = v_pages;
   a.lens = static_cast<const int32_t*>(lens);
-  a.scale = tp::paged::scale_of(desc) * tp::paged::kLog2e;
+  a.scale = tp::paged::scale_of(desc);
   const DecodePlan p = decode_plan(a.c, desc->dtype);
   char* ws = static_cast<char*>(workspace);
   a.lse = static_cast<float*>(lse ? lse : ws + w.lse);
