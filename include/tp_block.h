@@ -311,7 +311,10 @@ tp_status tp_rope(const tp_rope_desc* desc, int32_t dtype, int64_t T, int32_t n_
  * outside 0 .. n_pages-1, a sequence, a length) is never followed; the token or key is left out
  * and tp_check_device_error() reports TP_ERR_INDEX.
  * k_pages, v_pages: 16-byte aligned, strides multiples of 16 bytes; head_dim a multiple of 8 in
- * [8, 256]; dtype bf16 or fp32; b <= 65535 (the library's other decode calls' limit). */
+ * [8, 256]; dtype bf16 or fp32; b <= 65535 (the library's other decode calls' limit); n_q <= 65535;
+ * max_pages*page_size <= 2^30.
+ * The workspaces hold nothing between calls; calls that may run at the same time need one each, and
+ * their sizes are the current device's. */
 typedef struct {
   int64_t b;            /* sequences (rows of tables)                                         */
   int64_t n_pages;      /* pages in the pool                                                  */
@@ -323,7 +326,7 @@ typedef struct {
   int32_t head_dim;
   int32_t dtype;        /* tp_dtype                                                           */
   int32_t flags;        /* 0                                                                  */
-  float scale;          /* softmax scale; 0 means 1/sqrt(head_dim)                            */
+  float scale;          /* softmax scale, >= 0; 0 means 1/sqrt(head_dim)                      */
   int32_t reserved;
 } tp_paged_desc;
 
@@ -350,11 +353,14 @@ tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, const void* s
  *   score: NULL or fp32 [b][n_kv][max_pages*page_size]; the weights that the group's query heads
  *   gave to each key are added: score[i][g][n] += sum_j w_n(i, j), n < lens[i]; other entries stay
  *   as they are.
+ * Scores, softmax statistics, weights and sums are fp32 (bf16 products are exact, the weights enter
+ * the second product with 16 bits, fp32 products are taken from numbers cut into three bf16 parts
+ * where a group has more than four heads); o is rounded once.  A key whose score is -infinity has
+ * weight 0; if all scores are, o is NaN; a NaN key or an infinite value gives NaN where it is used.
  * The sum over the keys is split over the SMs and joined in a fixed order: equal calls on equal
  * devices give equal results.  Slots at and past lens[i] are not read.
- * workspace: tp_attn_decode_paged_workspace(desc, score != NULL) bytes, 16-byte aligned; its
- * contents need not survive between calls.  It grows with b * n_q * max_pages * page_size
- * where score is given. */
+ * workspace: tp_attn_decode_paged_workspace(desc, score != NULL) bytes, 16-byte aligned.  It grows
+ * with b * n_q * max_pages * page_size where score is given. */
 size_t tp_attn_decode_paged_workspace(const tp_paged_desc* desc, int32_t with_score);
 tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_head_rows* q,
                                const void* k_pages, const void* v_pages, const void* tables,
@@ -370,7 +376,8 @@ tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_head_rows* q,
  *   min(lens, budget) (may be lens); keep: NULL or int32 [b][n_kv][budget], the kept slots in
  *   ascending order (a sequence within the budget: 0 .. lens-1, then -1).
  * 1 <= budget <= max_pages*page_size, 0 <= recent <= budget.  The pages of a sequence that is cut
- * must not be shared.  Pages past slot budget-1 are free afterwards.
+ * must not be shared.  Pages past slot budget-1 are free afterwards.  A row whose page is outside the
+ * pool is not moved.
  * workspace: tp_kv_evict_paged_workspace(desc, budget) bytes, 16-byte aligned. */
 size_t tp_kv_evict_paged_workspace(const tp_paged_desc* desc, int32_t budget);
 tp_status tp_kv_evict_paged(const tp_paged_desc* desc, void* score, const void* lens,

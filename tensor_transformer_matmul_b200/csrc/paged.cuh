@@ -44,8 +44,9 @@ inline tp_status check_desc(const tp_paged_desc* d, View* v) {
   if (d->flags != 0) return set_error(TP_ERR_INVALID_ARG, "unknown flags");
   if (d->page_size < 1 || d->n_pages < 1 || d->n_pages > INT32_MAX || d->max_pages < 1)
     return set_error(TP_ERR_SHAPE, "page_size, n_pages and max_pages must be >= 1");
-  if (d->max_pages > (INT32_MAX - 1024) / d->page_size)
-    return set_error(TP_ERR_SHAPE, "max_pages * page_size must fit in 31 bits");
+  // (slots, and what a kernel adds to them for its steps, are 32-bit numbers)
+  if (d->max_pages > (1 << 30) / d->page_size)
+    return set_error(TP_ERR_SHAPE, "max_pages * page_size must be <= 2^30");
   if (!(d->scale >= 0.f) || !std::isfinite(d->scale))
     return set_error(TP_ERR_INVALID_ARG, "scale must be finite and >= 0");
   v->b = d->b;

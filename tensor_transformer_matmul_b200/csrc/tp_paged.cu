@@ -34,8 +34,9 @@ tp_status check_vec_rows(const tp_head_rows* r, int64_t T, int heads, int hd, in
 tp::rope::Rows rows_of(const tp_head_rows* r) { return {r->data, r->token_stride, r->head_stride}; }
 
 // ---- decode attention: which kernel, and its workspace ----
-// fp32 groups of up to this many heads multiply on the SIMT units
-constexpr int kSimtHeads = 1;
+// fp32 groups of up to this many heads multiply on the SIMT units (16 x 4000 keys, 4 heads of 128 dims
+// to a group: 63 us, 71 on the matrix instructions; 8 heads, one sequence group of 1123: 33 and 23)
+constexpr int kSimtHeads = 4;
 
 // heads of a tile and blocks of a split launch per SM: of the padded head size and the group
 struct DecodePlan {
@@ -47,7 +48,7 @@ DecodePlan decode_plan(const tp::paged::View& c, int dtype) {
   DecodePlan p;
   p.hdp = c.hd <= 64 ? 64 : c.hd <= 128 ? 128 : 256;
   if (dtype == TP_BF16) p.heads = c.group > 8 && p.hdp < 256 ? 16 : 8;
-  else p.heads = c.group <= kSimtHeads ? c.group : c.group > 8 && p.hdp < 256 ? 16 : 8;
+  else p.heads = c.group == 1 ? 1 : c.group <= kSimtHeads ? 4 : c.group > 8 && p.hdp < 256 ? 16 : 8;
   p.tiles = static_cast<int>(tp::ceil_div(c.group, p.heads));
   // One block per (sequence, KV head, head tile) or runs of equal length?  A block alone streams
   // about 0.1 TB/s; a split launch costs about 7 us more (the cuts' joins, a second kernel) but no
@@ -57,9 +58,9 @@ DecodePlan decode_plan(const tp::paged::View& c, int dtype) {
   // split: 1 x 700 keys 7.3 / 10.2 us, 1 x 4000 24.8 / 14.2, 16 ragged up to 1500 14.8 / 21.8,
   // 16 up to 4096 29.6 / 35.2, 64 up to 700 26 / 40, 16 up to 8000 56 / 58.
   const int64_t blocks = c.b * c.n_kv * p.tiles;
-  // (fp32 groups compute about four times as long per byte: 3 x 1123 keys of 64 / 8 fp32 heads of 128
-  // dims 23.5 us whole.)
-  const int64_t row = c.cap * c.hd * 2 * tp::elem_bytes(dtype) * (dtype == TP_F32 && p.heads > kSimtHeads ? 4 : 1);
+  // (an fp32 group computes two or four times as long per byte: 3 x 1123 keys of 64 / 8 fp32 heads of
+  // 128 dims 23.5 us whole, 22.2 split; 16 x 4000 of 32 / 8 heads of 64 dims 55 us whole.)
+  const int64_t row = c.cap * c.hd * 2 * tp::elem_bytes(dtype) * (dtype == TP_F32 && p.heads > 1 ? p.heads > 4 ? 4 : 2 : 1);
   p.whole = row <= (3 << 18) || (row <= (5 << 19) && blocks * 3 >= tp::num_sms());
   p.runs = tp::num_sms() * tp::paged::split_blocks(128 * p.hdp);   // (all engines' rings)
   return p;
@@ -304,6 +305,7 @@ extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_he
        ? (p.heads == 8 ? launch_decode<Mma<H, 1>>(a, p, s)                                       \
                        : launch_decode<Mma<H, H == 256 ? 1 : 2>>(a, p, s))                       \
        : (p.heads == 1 ? launch_decode<Simt<H, 1>>(a, p, s)                                      \
+                       : p.heads == 4 ? launch_decode<Simt<H, 4>>(a, p, s)                       \
                        : p.heads == 8 ? launch_decode<MmaF32<H, 1>>(a, p, s)                     \
                                       : launch_decode<MmaF32<H, H == 256 ? 1 : 2>>(a, p, s)))
   st = p.hdp == 64 ? TP_DECODE(64) : p.hdp == 128 ? TP_DECODE(128) : TP_DECODE(256);

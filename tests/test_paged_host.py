@@ -53,7 +53,7 @@ def test_status_string(lib):
 @pytest.mark.parametrize("bad", [
     dict(b=-1), dict(b=65536), dict(n_q=0), dict(n_kv=0), dict(n_q=7), dict(hd=4), dict(hd=12),
     dict(hd=264), dict(page=0), dict(n_pages=0), dict(max_pages=0),
-    dict(n_pages=1 << 31), dict(max_pages=1 << 28, page=16),
+    dict(n_pages=1 << 31), dict(max_pages=1 << 28, page=16), dict(max_pages=(1 << 26) + 1, page=16),
 ])
 def test_paged_shapes(lib, bad):
     d = _paged(lib, **bad)
