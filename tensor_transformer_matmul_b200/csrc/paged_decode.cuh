@@ -922,45 +922,59 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
 
-// units per run: at least min_units, so that short work is not cut into parts that cost more to
-// join than to compute
-__device__ __forceinline__ int64_t units_per_run(const DecodeArgs& a, int64_t units) {
-  const int64_t even = quotient(units + a.runs - 1, a.runs);
-  return even > a.min_units ? even : a.min_units;
-}
-
-// One block per run of units.
+// One block per run of units.  A run that ends one row of keys and begins the next passes over two
+// parts, one after the other; where there are few rows (a quarter of the runs at most) every row is
+// given a whole number of runs instead, its last one partly empty, and no run has two parts.
 template <typename E>
 __global__ void __launch_bounds__(split_warps(ring_bytes<E>()) * 32, split_blocks(ring_bytes<E>()))
     decode_split_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int W = split_warps(ring_bytes<E>());
   extern __shared__ __align__(128) char smem[];
-  __shared__ int64_t s_sum[W], s_seq, s_first;
+  __shared__ int64_t s_sum[2][W], s_seq, s_first;
   pdl_wait();
   pdl_trigger();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t tiles = static_cast<int64_t>(a.c.n_kv) * a.tiles;
-  auto chunks = [&](int64_t seq) { return (a.c.keys(a.lens, seq) + kChunk - 1) / kChunk; };
-  // units before this thread's sequences
   const int64_t per_thread = (a.c.b + W * 32 - 1) / (W * 32);
   const int64_t q0 = min(tid * per_thread, a.c.b), q1 = min(q0 + per_thread, a.c.b);
-  int64_t sum = 0;
-  for (int64_t s = q0; s < q1; ++s) sum += chunks(s);
-  int64_t x = sum;
+  int64_t grain = 1;                             // a row's units are a multiple of this
+  auto chunks = [&](int64_t seq) {
+    const int64_t n = (a.c.keys(a.lens, seq) + kChunk - 1) / kChunk;
+    return grain == 1 ? n : quotient(n + grain - 1, grain) * grain;
+  };
+  // units of this thread's sequences, before them, and of all
+  int64_t sum, before, total;
+  auto count = [&](int64_t* s_part) {
+    sum = 0;
+    for (int64_t s = q0; s < q1; ++s) sum += chunks(s);
+    int64_t x = sum;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_sum[warp] = x;
-  __syncthreads();
-  int64_t before = x - sum, total = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_part[warp] = x;
+    __syncthreads();
+    before = x - sum;
+    total = 0;
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) before += s_part[w];
+      total += s_part[w];
+    }
+  };
+  count(s_sum[0]);
+  // units of a run: at least min_units, so that short work is not cut into parts that cost more to
+  // join than to compute
+  const int64_t rows = a.c.b * tiles;
+  const bool aligned = rows * 4 <= a.runs;
+  const int64_t cuts = aligned ? a.runs - rows : a.runs;
+  const int64_t per = max(quotient(total * tiles + cuts - 1, cuts), a.min_units);
+  if (aligned) {
+    grain = per;
+    count(s_sum[1]);
   }
-  const int64_t units = total * tiles, per = units_per_run(a, units);
+  const int64_t units = total * tiles;
   const int64_t u0 = blockIdx.x * per, u1 = min(u0 + per, units);
   if (blockIdx.x == 0) {
     int64_t at = before;
