@@ -15,7 +15,8 @@
 //     operands of two instructions as they lie; values are paired over two keys by byte permutes.
 //     Larger instructions (tcgen05, 64 rows or more) would need the rows staged in the layouts that
 //     their descriptors know and gain nothing on a stream that memory bounds.
-//   * fp32: products in fp32 on the SIMT units.
+//   * fp32: products in fp32 on the SIMT units;
+//     groups of more than four heads use the matrix instructions on numbers cut into three.
 //
 // Split: a unit is 32 keys of one (sequence, KV head, tile of query heads); the units of the whole
 // batch lie in one line, cut into equal runs, one per block of a grid that fills the GPU once.  So
@@ -23,6 +24,10 @@
 // device knows).  A run that holds the whole of a (sequence, head) writes its output; the others
 // leave (m, l, o) for join_kernel.  Caches of short rows use one block per (sequence, head) and no
 // second launch.
+//
+// Measured (64 query / 8 KV heads of 128 bf16 dims, from DRAM): 32 ragged sequences of up to 16384
+// keys 198 us, 6.2 TB/s; one of 131071 91 us, 5.9 TB/s; 16 ragged of up to 4096 30 us, 4.9 TB/s (one
+// wave of unequal blocks); one of 200 4.7 us (latency of the lookups and copies).
 #pragma once
 
 #include "paged.cuh"
@@ -82,7 +87,7 @@ __device__ __forceinline__ float base_of(float m) { return m == -INFINITY ? 0.f 
 // eight lanes at a time, then touches all banks once.
 __device__ __forceinline__ int swizzle(int row) { return (((row >> 2) ^ row) & 1) << 2 | (row & 2); }
 
-// ---- the two ways to multiply; lane = 4 g + t ----
+// ---- the ways to multiply; lane = 4 g + t ----
 // bf16: NT tiles of 8 heads; a step is 16 keys.  A lane's scores: keys g and g + 8, heads
 // 8 nt + 2 t and the next.
 template <int HDP_, int NT>
@@ -419,7 +424,7 @@ struct MmaF32 {
   }
 };
 
-// fp32: G heads (1, 4 or 8); a step is 8 keys.  Four lanes share a key's dims and then its heads:
+// fp32: G heads (1 or 4); a step is 8 keys.  Four lanes share a key's dims and then its heads:
 // a lane's scores: key g, heads HPL t and the next (G == 1: all four the same).  A lane owns four
 // dims of the output (HDP 256: eight; HDP 64: of every other key).
 template <int HDP_, int G>

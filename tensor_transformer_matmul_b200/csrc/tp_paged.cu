@@ -35,7 +35,7 @@ tp::rope::Rows rows_of(const tp_head_rows* r) { return {r->data, r->token_stride
 
 // ---- decode attention: which kernel, and its workspace ----
 // fp32 groups of up to this many heads multiply on the SIMT units (16 x 4000 keys, 4 heads of 128 dims
-// to a group: 63 us, 71 on the matrix instructions; 8 heads, one sequence group of 1123: 33 and 23)
+// to a group: 63 us, 71 on the matrix instructions; 3 x 1123 keys, 8 heads: 33 and 23 us)
 constexpr int kSimtHeads = 4;
 
 // heads of a tile and blocks of a split launch per SM: of the padded head size and the group
@@ -51,17 +51,17 @@ DecodePlan decode_plan(const tp::paged::View& c, int dtype) {
   else p.heads = c.group == 1 ? 1 : c.group <= kSimtHeads ? 4 : c.group > 8 && p.hdp < 256 ? 16 : 8;
   p.tiles = static_cast<int>(tp::ceil_div(c.group, p.heads));
   // One block per (sequence, KV head, head tile) or runs of equal length?  A block alone streams
-  // about 0.1 TB/s; a split launch costs about 7 us more (the cuts' joins, a second kernel) but no
+  // about 0.1 TB/s; a split launch costs about 5 us more (the cuts' joins, a second kernel) but no
   // row, however long, then holds the others up.  The host knows the rows' room, not their lengths,
-  // so whole rows are for room that one block reads in 10 us, or in 25 us where there are enough
+  // so whole rows are for room that one block reads in 8 us, or in 25 us where there are enough
   // blocks to keep a third of the SMs busy.  Measured on 64 / 8 bf16 heads of 128 dims, whole and
-  // split: 1 x 700 keys 7.3 / 10.2 us, 1 x 4000 24.8 / 14.2, 16 ragged up to 1500 14.8 / 21.8,
-  // 16 up to 4096 29.6 / 35.2, 64 up to 700 26 / 40, 16 up to 8000 56 / 58.
+  // split: 1 x 700 keys 7.8 / 9.8 us, 1 x 1000 9.6 / 10.0, 1 x 1500 11.7 / 10.1, 1 x 4000 24.8 / 13.2,
+  // 16 ragged up to 1500 15 / 22, 16 up to 4096 30 / 35, 64 up to 700 27 / 40.
   const int64_t blocks = c.b * c.n_kv * p.tiles;
-  // (an fp32 group computes two or four times as long per byte: 3 x 1123 keys of 64 / 8 fp32 heads of
-  // 128 dims 23.5 us whole, 22.2 split; 16 x 4000 of 32 / 8 heads of 64 dims 55 us whole.)
+  // (An fp32 group computes two or four times as long per byte: 3 x 1123 keys of 64 / 8 fp32 heads of
+  // 128 dims 23.5 us whole, 17.8 split; 16 x 4000 of 32 / 8 heads of 64 dims 55 and 39 us.)
   const int64_t row = c.cap * c.hd * 2 * tp::elem_bytes(dtype) * (dtype == TP_F32 && p.heads > 1 ? p.heads > 4 ? 4 : 2 : 1);
-  p.whole = row <= (3 << 18) || (row <= (5 << 19) && blocks * 3 >= tp::num_sms());
+  p.whole = row <= (5 << 17) || (row <= (5 << 19) && blocks * 3 >= tp::num_sms());
   p.runs = tp::num_sms() * tp::paged::split_blocks(128 * p.hdp);   // (all engines' rings)
   return p;
 }
@@ -88,11 +88,24 @@ DecodeWs decode_ws(const tp::paged::View& c, int dtype, bool with_score) {
   return w;
 }
 
+// Lets a kernel use ``bytes`` of dynamic shared memory; done: per device, whether it may already.
+template <typename K>
+tp_status allow_smem(K* kern, int bytes, int (&done)[64]) {
+  int dev = 0;
+  TP_CUDA_TRY(cudaGetDevice(&dev));
+  if (dev < 64 && done[dev]) return TP_OK;
+  TP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  if (dev < 64) done[dev] = 1;
+  return TP_OK;
+}
+
 template <typename E, int W>
 tp_status launch_whole(const tp::paged::DecodeArgs& a, dim3 grid, cudaStream_t s) {
   constexpr int smem = tp::paged::decode_smem<E>(W);
   auto* whole = tp::paged::decode_whole_kernel<E, W>;
-  TP_CUDA_TRY(cudaFuncSetAttribute(whole, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  static int done[64];
+  const tp_status st = allow_smem(whole, smem, done);
+  if (st != TP_OK) return st;
   TP_LAUNCH_PDL(whole, grid, dim3(W * 32), smem, s, a);
   return TP_OK;
 }
@@ -113,7 +126,9 @@ tp_status launch_decode(const tp::paged::DecodeArgs& a, const DecodePlan& p, cud
   }
   constexpr int smem = decode_smem<E>(kSplit);
   auto* split = decode_split_kernel<E>;
-  TP_CUDA_TRY(cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  static int done[64];
+  const tp_status st = allow_smem(split, smem, done);
+  if (st != TP_OK) return st;
   TP_LAUNCH_PDL(split, dim3(static_cast<unsigned>(a.runs)), dim3(kSplit * 32), smem, s, a);
   auto* join = join_kernel<typename E::T, E::kHeads>;
   TP_LAUNCH_PDL(join, dim3(static_cast<unsigned>(a.c.n_q), static_cast<unsigned>(a.c.b)), dim3(128), 0, s, a);
@@ -372,9 +387,9 @@ extern "C" tp_status tp_kv_evict_paged(const tp_paged_desc* desc, void* score, c
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   {
     tp::ProfScope prof(s, "kv_evict_select");
+    static int done[64];
+    if ((st = allow_smem(tp::paged::evict_select_kernel, tp::paged::kEvictRoom * 4, done)) != TP_OK) return st;
     const int smem = a.room * 4;
-    TP_CUDA_TRY(cudaFuncSetAttribute(tp::paged::evict_select_kernel,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     TP_LAUNCH_PDL(tp::paged::evict_select_kernel,
                   dim3(static_cast<unsigned>(desc->n_kv), static_cast<unsigned>(desc->b)),
                   dim3(tp::paged::kEvictThreads), smem, s, a);
@@ -383,8 +398,8 @@ extern "C" tp_status tp_kv_evict_paged(const tp_paged_desc* desc, void* score, c
   const dim3 grid(static_cast<unsigned>(2 * a.strips), static_cast<unsigned>(desc->n_kv),
                   static_cast<unsigned>(desc->b));
   constexpr int smem = tp::paged::kMoveWarps * tp::paged::kMoveRing;
-  TP_CUDA_TRY(cudaFuncSetAttribute(tp::paged::evict_move_kernel,
-                                   cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  static int done[64];
+  if ((st = allow_smem(tp::paged::evict_move_kernel, smem, done)) != TP_OK) return st;
   TP_LAUNCH_PDL(tp::paged::evict_move_kernel, grid, dim3(tp::paged::kMoveWarps * 32), smem, s, a, eb);
   return TP_OK;
 }
