@@ -370,7 +370,8 @@ tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_head_rows* q,
 /* Cut every sequence longer than budget back to budget keys.  Per (sequence, KV head) the last
  * `recent` keys stay, and of the others the budget - recent with the largest score (equal scores:
  * the lower slot; a NaN score counts as the smallest).  The kept keys, values and scores are
- * moved to slots 0 .. budget-1 in their order, in place; the slots behind keep their old contents.
+ * moved to slots 0 .. budget-1 in their order, in place; the slots behind keep their old contents
+ * (clear their scores before new keys that are put there gather weight).
  * Keys that were rotated keep their rotation.
  *   score: fp32 [b][n_kv][max_pages*page_size]; lens: int32 [b]; new_lens: int32 [b] receives
  *   min(lens, budget) (may be lens); keep: NULL or int32 [b][n_kv][budget], the kept slots in

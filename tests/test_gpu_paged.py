@@ -29,12 +29,12 @@ class Cache:
     """A pool whose pages are handed out in a shuffled order; what no sequence uses is NaN."""
 
     def __init__(self, lib, lens, n_q, n_kv, hd, page, dtype="bf16", seed=0, slot_major=False,
-                 extra=0, pad=0):
+                 extra=0, pad=0, width=0):
         g = torch.Generator().manual_seed(seed)
         self.lib, self.n_q, self.n_kv, self.hd, self.page = lib, n_q, n_kv, hd, page
         self.dtype, self.lens_l, b = dtype, list(lens), len(lens)
         used = [-(-(n + extra) // page) for n in lens]
-        width, n_pages = max(max(used), 1) + 1, sum(used) + 3
+        width, n_pages = max(max(used) + 1, 2, width), sum(used) + 3
         order = torch.randperm(n_pages, generator=g).tolist()
         t = torch.full((b, width), -1, dtype=torch.int32)     # entries not in use: never read
         for i, u in enumerate(used):
@@ -84,6 +84,8 @@ class Cache:
         scale = self.desc.scale or self.hd ** -0.5
         group = self.n_q // self.n_kv
         o, lse = f64(o), f64(lse)
+        if before is not None:
+            got, was = f64(self.score), f64(before)
         for i, n in enumerate(lens):
             slots, pg, at = opaged.slots_of(tables, i, min(n, self.cap), self.page, kp.shape[0])
             if not len(slots):
@@ -104,11 +106,11 @@ class Cache:
                 tl = dz[:, 0] + (n + 8) * U + 4 * U * np.abs(rl[i, hs])
                 assert (np.abs(lse[i, hs] - rl[i, hs]) <= tl).all(), (i, g)
                 if before is not None:
-                    want = f64(before)[i, g].copy()
+                    want = was[i, g].copy()
                     want[:rw[i].shape[1]] += rw[i][g]
                     tol = np.zeros(self.cap)
                     tol[slots] = (w * (2 * dz + (2 * n + 16) * U)).sum(0) + U * np.abs(want[slots])
-                    assert (np.abs(f64(self.score)[i, g] - want) <= tol).all(), (i, g)
+                    assert (np.abs(got[i, g] - want) <= tol).all(), (i, g)
         if before is not None:      # empty sequences and what lies behind a sequence
             for i, n in enumerate(lens):
                 assert torch.equal(self.score[i, :, n:], before[i, :, n:])
@@ -155,6 +157,28 @@ def test_decode(lib, lens, n_q, n_kv, hd, page, dtype, slot_major):
     lib.tp_check_device_error()
 
 
+@pytest.mark.parametrize("lens,n_q,n_kv,hd,page,dtype", DECODE)
+def test_decode_wide_tables(lib, lens, n_q, n_kv, hd, page, dtype):
+    # tables with room for rows far longer than the sequences: the work is cut into runs, which end
+    # anywhere in a sequence, hold several short ones, and meet empty ones
+    c = Cache(lib, lens, n_q, n_kv, hd, page, dtype, width=60000 // page)
+    few = len(lens) * n_kv <= 40
+    before = c.score.clone() if few else None
+    o, lse = c.decode(with_score=few)
+    c.check(o, lse, before)
+    o2, lse2 = c.decode(with_score=False)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    lib.tp_check_device_error()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_decode_many_rows_in_runs(lib, dtype):
+    # more rows than runs, lengths around a unit's
+    lens = [(37 * i) % 101 for i in range(100)] + [1, 2500, 33]
+    c = Cache(lib, lens, 8, 4, 64, 16, dtype, width=2000)
+    c.check(*c.decode(with_score=False), None)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_decode_long(lib, dtype):
     # one sequence over every SM, and lengths that end anywhere in the split
@@ -189,25 +213,28 @@ def test_decode_extreme_values(lib):
     c.check(*c.decode(), before)
 
 
+@pytest.mark.parametrize("width", [0, 4000])     # whole rows; runs, some of them without a weight
 @pytest.mark.parametrize("n_q,dtype", [(4, "bf16"), (4, "f32"), (1, "f32"), (16, "f32")])
-def test_decode_infinite_keys(lib, n_q, dtype):
+def test_decode_infinite_keys(lib, n_q, dtype, width):
     # a key with a score of -infinity has weight 0; all of them: no softmax (NaN), lse -infinity
-    c = Cache(lib, [100, 40], n_q, 1, 64, 16, dtype)
+    a, b = (1000, 400) if width else (100, 40)
+    c = Cache(lib, [a, b], n_q, 1, 64, 16, dtype, width=width)
     c.q[..., 0] = 1.0
-    kp, vp, tables = c.host()
-    hit = [s for s in range(100) if s % 3 == 0 or s < 40]
-    for i, s in [(0, s) for s in hit] + [(1, s) for s in range(40)]:
-        c.kp[tables[i][s // 16], 0, s % 16, 0] = -float("inf")
+    tables = c.tables.cpu().numpy()
+    hit = [s for s in range(a) if s % 3 == 0 or s < b]
+    for i, at in ((0, torch.tensor(hit)), (1, torch.arange(b))):
+        c.kp[c.tables[i, (at // 16).to(dev())].long(), 0, (at % 16).to(dev()), 0] = -float("inf")
     before = c.score.clone()
     o, lse = c.decode()
     assert torch.isnan(o[1]).all() and torch.isneginf(lse[1]).all()
-    assert torch.isnan(c.score[1, 0, :40]).all()
-    kp, vp, tables = c.host()
+    assert torch.isnan(c.score[1, 0, :b]).all()
+    kp, vp = f64(c.kp), f64(c.vp)
+    s = np.arange(a)
+    k, v = kp[tables[0][s // 16], 0, s % 16], vp[tables[0][s // 16], 0, s % 16]
     for j in range(n_q):
-        z = np.array([kp[tables[0][s // 16], 0, s % 16] @ f64(c.q)[0, j] / 8.0 for s in range(100)])
+        z = k @ f64(c.q)[0, j] / 8.0
         e = np.exp(z - z.max())
-        want = (e / e.sum()) @ np.stack([vp[tables[0][s // 16], 0, s % 16] for s in range(100)])
-        assert np.allclose(f64(o)[0, j], want, rtol=2e-2, atol=2e-2)
+        assert np.allclose(f64(o)[0, j], (e / e.sum()) @ v, rtol=2e-2, atol=2e-2)
     assert torch.equal(c.score[0, 0, hit], before[0, 0, hit])
     # NaN in a key: its sequence and KV head give NaN, others do not
     c2 = Cache(lib, [100, 40], 2 * n_q, 2, 64, 16, dtype)
