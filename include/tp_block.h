@@ -289,8 +289,8 @@ tp_status tp_rope_freqs(const tp_rope_desc* desc, void* freqs, void* stream);
 /* out = the rotation of x; inverse != 0: its gradient, m * R(-a) x (the transpose, so with
  * x = dL/dout the result is dL/dx).  x and out: T tokens of n_heads heads of head_dim elements of
  * dtype; out may be x with the same strides (in place), and must not overlap it otherwise.
- * positions: int32 [T] (any sign).  n_heads <= 65535.  Any element alignment and any head_dim in [rot_dim, 1024];
- * 16-byte aligned rows with rot_dim/2 (half) or rot_dim (interleaved) a multiple of 16 bytes are
+ * positions: int32 [T] (any sign).  n_heads <= 65535.  Any element alignment and any head_dim in
+ * [rot_dim, 1024]; 16-byte aligned rows with rot_dim/2 (half) or rot_dim (interleaved) a multiple of 16 bytes are
  * moved in 16-byte vectors. */
 tp_status tp_rope(const tp_rope_desc* desc, int32_t dtype, int64_t T, int32_t n_heads,
                   int32_t head_dim, const tp_head_rows* x, const void* positions,

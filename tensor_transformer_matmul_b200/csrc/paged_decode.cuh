@@ -234,8 +234,8 @@ __device__ __forceinline__ void cut3(float a, float b, uint32_t (&w)[3]) {
 // one before, and of the nine products of two sums the six largest are taken; what is left out is
 // below 2^-25 of the product.  The instructions' own sums are cut off, not rounded, so they run over
 // one step or 16 dims only, and fp32 additions join them.  A cut costs 5.5 instructions a number once,
-// plain fp32 products one a head.  Layout as above with four dims to
-// 16 bytes; the queries' parts lie in shared memory as the lanes' operands.
+// plain fp32 products one a head.  Layout as above with four dims to 16 bytes; the queries' parts lie
+// in shared memory as the lanes' operands.
 template <int HDP_, int NT>
 struct MmaF32 {
   using T = float;
@@ -425,7 +425,7 @@ struct MmaF32 {
 };
 
 // fp32: G heads (1 or 4); a step is 8 keys.  Four lanes share a key's dims and then its heads:
-// a lane's scores: key g, heads HPL t and the next (G == 1: all four the same).  A lane owns four
+// a lane's scores: key g, head t (G == 1: all four the same).  A lane owns four
 // dims of the output (HDP 256: eight; HDP 64: of every other key).
 template <int HDP_, int G>
 struct Simt {
@@ -929,7 +929,8 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 
 // One block per run of units.  A run that ends one row of keys and begins the next passes over two
 // parts, one after the other; where there are few rows (a quarter of the runs at most) every row is
-// given a whole number of runs instead, its last one partly empty, and no run has two parts.
+// given a whole number of runs instead, its last one partly empty, and no run has two parts (3 x 1123
+// fp32 keys, 24 rows on 296 runs: 22.9 -> 17.8 us; 16 x 4000, 128 rows on 148 runs, would lose: 76 -> 95).
 template <typename E>
 __global__ void __launch_bounds__(split_warps(ring_bytes<E>()) * 32, split_blocks(ring_bytes<E>()))
     decode_split_kernel(const __grid_constant__ DecodeArgs a) {
