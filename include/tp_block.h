@@ -290,8 +290,8 @@ tp_status tp_rope_freqs(const tp_rope_desc* desc, void* freqs, void* stream);
  * x = dL/dout the result is dL/dx).  x and out: T tokens of n_heads heads of head_dim elements of
  * dtype; out may be x with the same strides (in place), and must not overlap it otherwise.
  * positions: int32 [T] (any sign).  n_heads <= 65535.  Any element alignment and any head_dim in
- * [rot_dim, 1024]; 16-byte aligned rows with rot_dim/2 (half) or rot_dim (interleaved) a multiple of 16 bytes are
- * moved in 16-byte vectors. */
+ * [rot_dim, 1024]; 16-byte aligned rows with rot_dim/2 (half) or rot_dim (interleaved) a multiple of 16
+ * bytes are moved in 16-byte vectors (half: also 8-byte ones). */
 tp_status tp_rope(const tp_rope_desc* desc, int32_t dtype, int64_t T, int32_t n_heads,
                   int32_t head_dim, const tp_head_rows* x, const void* positions,
                   const void* freqs, int32_t inverse, const tp_head_rows* out, void* stream);

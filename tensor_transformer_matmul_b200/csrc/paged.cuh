@@ -112,6 +112,10 @@ struct Target {
   }
 };
 
+inline bool vector_rows(const Target& t, int eb, int bytes) {   // (the cache's strides fit 16)
+  return rope::vector_rows(t.k, eb, bytes) && rope::vector_rows(t.v, eb, bytes);
+}
+
 // ---------------------------------------------------------------------------------- evict
 struct EvictArgs {
   View c;

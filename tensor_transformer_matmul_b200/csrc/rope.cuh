@@ -89,16 +89,36 @@ struct Share {
 };
 constexpr int kRotateWarps = 4, kRotateSteps = 24, kRotateRing = 8;
 
-// 16-byte vectors: an item is one vector of a row (interleaved pairs, or dims that pass through) or
+// The vectors that rows move in: 16 bytes, or 8 where halves of a rotation are no multiple of 16.
+template <int kBytes> struct Vec;
+template <> struct Vec<16> {
+  using type = uint4;
+  __device__ __forceinline__ static void copy(uint32_t dst, const void* src) { copy16(dst, src, true); }
+  __device__ __forceinline__ static type lds(uint32_t a) { return lds16(a); }
+};
+template <> struct Vec<8> {
+  using type = uint2;
+  __device__ __forceinline__ static void copy(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  }
+  __device__ __forceinline__ static type lds(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
+    return r;
+  }
+};
+
+// Vectors: an item is one vector of a row (interleaved pairs, or dims that pass through) or
 // two, half a rotation apart.  A warp has a slice of a token's rows, a lane the same item of every
 // step-th row.  The vectors are copied asynchronously into a ring of shared memory, eight of a lane
 // in flight, each lane reading back what it copied itself; while the first ones fly the warp
 // computes the token's sines and cosines (64-bit products up to the reduced angle), each once, for
 // all rows of the slice.  No warp waits for another.  Bound by the bytes moved.
-template <typename T, int kVecs, typename Cache>
+template <typename T, int kVecs, int kBytes, typename Cache>
 __global__ void __launch_bounds__(kRotateWarps * 32) rotate_rows_kernel(
     const __grid_constant__ Args a, const __grid_constant__ Cache c, const __grid_constant__ Share sh) {
-  constexpr int VE = 16 / sizeof(T), kPairs = VE * kVecs / 2, kDepth = kRotateRing / kVecs;
+  using V = typename Vec<kBytes>::type;
+  constexpr int VE = kBytes / sizeof(T), kPairs = VE * kVecs / 2, kDepth = kRotateRing / kVecs;
   constexpr int kWide = kPairs < 4 ? 2 : 4;
   extern __shared__ __align__(16) char smem[];           // [warp][ring][32] vectors, [warp][2][half]
   pdl_wait();
@@ -128,8 +148,8 @@ __global__ void __launch_bounds__(kRotateWarps * 32) rotate_rows_kernel(
       const T* from = j < 0 ? xq + row * a.x.hs : j < c.n_kv ? xk + j * c.k.hs : xv + (j - c.n_kv) * c.v.hs;
       const uint32_t to = ring + (s % kDepth) * (kVecs * 512);
       if (row < r1) {
-        copy16(to, from, true);
-        if (kVecs == 2 && pair) copy16(to + 512, from + a.half, true);
+        Vec<kBytes>::copy(to, from);
+        if (kVecs == 2 && pair) Vec<kBytes>::copy(to + 512, from + a.half);
       }
       copy_commit();
     };
@@ -169,15 +189,15 @@ __global__ void __launch_bounds__(kRotateWarps * 32) rotate_rows_kernel(
       copy_wait<kDepth - 1>();
       if (row < r1 && (j < 0 || slot >= 0)) {
         const uint32_t at = ring + (s % kDepth) * (kVecs * 512);
-        uint4 x[kVecs];
-        x[0] = lds16(at);
-        if (kVecs == 2 && pair) x[kVecs - 1] = lds16(at + 512);
+        V x[kVecs];
+        x[0] = Vec<kBytes>::lds(at);
+        if (kVecs == 2 && pair) x[kVecs - 1] = Vec<kBytes>::lds(at + 512);
         T* to = j < 0 ? oq + row * a.out.hs : j < c.n_kv ? ok + j * c.head_stride
                                                          : ov + (j - c.n_kv) * c.head_stride;
         if (pair && j < c.n_kv) {
-          T y[VE * kVecs];
+          alignas(16) T y[VE * kVecs];
 #pragma unroll
-          for (int v = 0; v < kVecs; ++v) *reinterpret_cast<uint4*>(y + v * VE) = x[v];
+          for (int v = 0; v < kVecs; ++v) *reinterpret_cast<V*>(y + v * VE) = x[v];
 #pragma unroll
           for (int i = 0; i < kPairs; ++i) {
             const int e1 = kVecs == 2 ? i : 2 * i, e2 = kVecs == 2 ? VE + i : 2 * i + 1;
@@ -186,10 +206,10 @@ __global__ void __launch_bounds__(kRotateWarps * 32) rotate_rows_kernel(
             y[e2] = from_f<T>(x1 * si[i] + x2 * co[i]);
           }
 #pragma unroll
-          for (int v = 0; v < kVecs; ++v) x[v] = *reinterpret_cast<const uint4*>(y + v * VE);
+          for (int v = 0; v < kVecs; ++v) x[v] = *reinterpret_cast<const V*>(y + v * VE);
         }
-        *reinterpret_cast<uint4*>(to) = x[0];
-        if (kVecs == 2 && pair) *reinterpret_cast<uint4*>(to + a.half) = x[kVecs - 1];
+        *reinterpret_cast<V*>(to) = x[0];
+        if (kVecs == 2 && pair) *reinterpret_cast<V*>(to + a.half) = x[kVecs - 1];
       }
       issue(s + kDepth);
     }
@@ -304,18 +324,26 @@ inline tp_status check_pair(const tp_head_rows* x, const tp_head_rows* o, const 
   return TP_OK;
 }
 
-inline bool vector_rows(const Rows& r, int64_t unit) {
-  return !(reinterpret_cast<uintptr_t>(r.p) & 15) && r.ts % unit == 0 && r.hs % unit == 0;
+// rows that start on a multiple of ``bytes``
+inline bool vector_rows(const Rows& r, int eb, int bytes) {
+  return !(reinterpret_cast<uintptr_t>(r.p) % bytes) && r.ts * eb % bytes == 0 && r.hs * eb % bytes == 0;
 }
+inline bool vector_rows(const NoCache&, int, int) { return true; }
 
-// ``vectors``: the cache's rows (if any) fit 16-byte vectors.
 template <typename T, typename Cache>
-inline tp_status launch_rows(const Args& a, const Cache& c, bool vectors, cudaStream_t s) {
-  constexpr int VE = 16 / sizeof(T);
-  const int vecs = a.interleaved ? 1 : 2, rot = 2 * a.half;
+inline tp_status launch_rows(const Args& a, const Cache& c, cudaStream_t s) {
+  const int vecs = a.interleaved ? 1 : 2, rot = 2 * a.half, eb = static_cast<int>(sizeof(T));
   const int64_t rows = a.heads + 2 * c.n_kv;
-  if (a.heads > 0) vectors = vectors && vector_rows(a.x, VE) && vector_rows(a.out, VE);
-  if (vectors && rot % (VE * vecs) == 0 && (a.hd - rot) % VE == 0) {
+  // 16-byte vectors where they fit, 8-byte ones for the halves they do not (a head of 80 bf16 dims, 40
+  // of them rotated: 1715 tokens of 80 rows 52 us by elements)
+  auto fits = [&](int bytes) {
+    const int VE = bytes / eb;
+    return rot % (VE * vecs) == 0 && (a.hd - rot) % VE == 0 && vector_rows(c, eb, bytes) &&
+           (a.heads == 0 || (vector_rows(a.x, eb, bytes) && vector_rows(a.out, eb, bytes)));
+  };
+  const int bytes = fits(16) ? 16 : !a.interleaved && fits(8) ? 8 : 0;
+  if (bytes) {
+    const int VE = bytes / eb;
     // in place the dims that pass through stay where they are
     const int pass = c.n_kv == 0 && a.x.p == a.out.p ? 0 : (a.hd - rot) / VE;
     const int64_t items = rot / (VE * vecs) + pass;
@@ -335,9 +363,11 @@ inline tp_status launch_rows(const Args& a, const Cache& c, bool vectors, cudaSt
     const dim3 g(static_cast<unsigned>(blocks)), threads(kRotateWarps * 32);
     const size_t smem = static_cast<size_t>(kRotateWarps) * (kRotateRing * 512 + a.half * 8);
     if (a.interleaved)
-      TP_LAUNCH_PDL((rotate_rows_kernel<T, 1, Cache>), g, threads, smem, s, a, c, sh);
+      TP_LAUNCH_PDL((rotate_rows_kernel<T, 1, 16, Cache>), g, threads, smem, s, a, c, sh);
+    else if (bytes == 16)
+      TP_LAUNCH_PDL((rotate_rows_kernel<T, 2, 16, Cache>), g, threads, smem, s, a, c, sh);
     else
-      TP_LAUNCH_PDL((rotate_rows_kernel<T, 2, Cache>), g, threads, smem, s, a, c, sh);
+      TP_LAUNCH_PDL((rotate_rows_kernel<T, 2, 8, Cache>), g, threads, smem, s, a, c, sh);
     return TP_OK;
   }
   const int64_t n = a.T * rows * (a.hd - a.half);

@@ -189,8 +189,8 @@ extern "C" tp_status tp_rope(const tp_rope_desc* desc, int32_t dtype, int64_t T,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   tp::ProfScope prof(s, "rope");
   const tp::rope::NoCache none{};
-  return dtype == TP_BF16 ? tp::rope::launch_rows<__nv_bfloat16>(a, none, true, s)
-                          : tp::rope::launch_rows<float>(a, none, true, s);
+  return dtype == TP_BF16 ? tp::rope::launch_rows<__nv_bfloat16>(a, none, s)
+                          : tp::rope::launch_rows<float>(a, none, s);
 }
 
 extern "C" tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, const void* seq_ids,
@@ -256,9 +256,8 @@ extern "C" tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, co
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   tp::ProfScope prof(s, "kv_append");
-  const bool vec = tp::rope::vector_rows(c.k, 16 / eb) && tp::rope::vector_rows(c.v, 16 / eb);
-  return desc->dtype == TP_BF16 ? tp::rope::launch_rows<__nv_bfloat16>(a, c, vec, s)
-                                : tp::rope::launch_rows<float>(a, c, vec, s);
+  return desc->dtype == TP_BF16 ? tp::rope::launch_rows<__nv_bfloat16>(a, c, s)
+                                : tp::rope::launch_rows<float>(a, c, s);
 }
 
 extern "C" size_t tp_attn_decode_paged_workspace(const tp_paged_desc* desc, int32_t with_score) {

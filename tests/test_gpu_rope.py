@@ -58,7 +58,8 @@ def test_frequencies(lib, R, scaling, factor):
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("T,H,hd,R", [(1, 1, 2, 2), (5, 3, 128, 128), (257, 9, 128, 64),
                                       (33, 2, 80, 80), (19, 7, 96, 48), (7, 72, 256, 256),
-                                      (3, 5, 50, 34), (130, 1, 1024, 1024), (700, 40, 64, 32)])
+                                      (3, 5, 50, 34), (130, 1, 1024, 1024), (700, 40, 64, 32),
+                                      (65, 9, 80, 40), (9, 2, 1024, 8)])
 def test_rotation(lib, T, H, hd, R, layout, dtype):
     x = rows(T + hd, T, H, hd, dtype=dtype)
     pos = torch.arange(T, dtype=torch.int32, device=dev()) * 37 - 11
