@@ -96,7 +96,7 @@ struct Mma {
   static constexpr int HDP = HDP_, kHeads = 8 * NT, kStep = 16, kOwn = 2 * NT, kKeys = 2;
   static constexpr int kRowBytes = HDP * 2, kStages = 2;
   static constexpr int kShared = 0;                 // block-wide and per-warp scratch
-  static constexpr bool kRedo = false;
+  static constexpr bool kRedo = false, kRedoApart = true;
   static constexpr int kWarpShared = 0;
   uint32_t q[HDP / 32][NT][4];
   float acc[HDP / 16][NT][4];
@@ -220,7 +220,7 @@ struct Mma {
 };
 
 // Two fp32 numbers as the sums of three bf16 numbers each (every remainder is exact; numbers that
-// round to an infinite bf16 have no parts).
+// round to an infinite bf16, those above 3.3895e38, have no parts).
 __device__ __forceinline__ void cut3(float a, float b, uint32_t (&w)[3]) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
@@ -243,7 +243,7 @@ struct MmaF32 {
   static constexpr int kRowBytes = HDP * 4, kStages = 1;
   static constexpr int kShared = HDP / 16 * NT * 3 * 256;      // [16 dims][tile][part][lane] pairs
   static constexpr int kWarpShared = 0;
-  static constexpr bool kRedo = true;
+  static constexpr bool kRedo = true, kRedoApart = true;
   float acc[HDP / 16][NT][4];
 
   __device__ __forceinline__ static int head(int i, int t) { return (i >> 1) * 8 + 2 * t + (i & 1); }
@@ -433,7 +433,7 @@ struct Simt {
   static constexpr int HDP = HDP_, kHeads = G, kStep = 8, kOwn = G >= 4 ? G / 4 : 1, kKeys = 1;
   static constexpr int kRowBytes = HDP * 4, kStages = 2;
   static constexpr int kShared = G * HDP * 4;
-  static constexpr bool kRedo = false;
+  static constexpr bool kRedo = false, kRedoApart = false;
   static constexpr int kWarpShared = 8 * G * 4;
   static constexpr int kLanes = HDP / 4 < 32 ? HDP / 4 : 32;   // lanes of a row of V
   static constexpr int kRows = 32 / kLanes;                    // rows of a copy of V
@@ -574,10 +574,87 @@ constexpr int decode_smem(int warps) {
   return warps * (ring_bytes<E>() + E::kWarpShared) + E::kShared + warps * E::kHeads * 8;
 }
 
-// Keys k0 .. k1-1 of (sequence, KV head g), heads j0 .. j0+heads-1: this warp's share of them.
-// On return the accumulators are in the warp's ring, its maxima and sums in sm / sl.
+// Outputs are summed with weights of up to e^kSlack before the division, and as sums of bf16 parts:
+// values near the largest number overflow there although their mean does not, and an infinite value
+// meets a second part of either sign or of 0.  A warp whose sums lie beyond kFarthest (or are not
+// numbers) takes those heads again in plain fp32 (redo_values), with weights that add up to 2^-14:
+// then no part exceeds kFarthest, nor does the sum of all parts (444 runs of 6 warps of two halves
+// each, or 12 warps) reach 2^127, and what is infinite or NaN in o is so in sum_n w_n v_n.
+constexpr float kFarthest = 20769187434139310514121985316880384.f;    // 2^114
+constexpr float kRedoShift = 9.7040605f;                               // 14 log 2
+template <int A, int B, int C>
+__device__ __forceinline__ bool beyond(const float (&acc)[A][B][C]) {
+  bool far = false;
+#pragma unroll
+  for (int i = 0; i < A; ++i)
+#pragma unroll
+    for (int n = 0; n < B; ++n)
+#pragma unroll
+      for (int r = 0; r < C; ++r) far |= !(fabsf(acc[i][n][r]) <= kFarthest);
+  return far;
+}
+// out [heads][HDP], sm, sl: the warp's sums, maxima and sums of weights of its keys of k0 .. k1-1
 template <typename E, int W>
-__device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq, int g, int j0,
+__device__ __forceinline__ void redo_values(const DecodeArgs& a, int64_t seq, int g, int j0, int heads,
+                                            int k0, int k1, float* out, float* sm, float* sl) {
+  using T = typename E::T;
+  constexpr int kDims = (E::HDP + 31) / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const T* qp = static_cast<const T*>(a.q.p) + seq * a.q.ts + j0 * a.q.hs;
+  const T* kp = static_cast<const T*>(a.kp) + g * a.c.head_stride;
+  const T* vp = static_cast<const T*>(a.vp) + g * a.c.head_stride;
+  const int32_t* table = a.c.tables + seq * a.c.max_pages;
+  const int hd = a.c.hd;
+  for (int h = 0; h < heads; ++h) {
+    const float m = sm[h], l = sl[h];
+    bool far = false;
+    for (int d = lane; d < hd; d += 32) far |= !(fabsf(out[h * E::HDP + d]) <= kFarthest);
+    // (without a sum there is no softmax, or NaN for every dim)
+    if (!__any_sync(0xffffffffu, far) || !(l > 0.f)) continue;
+    const float base = m + logf(l) + kRedoShift;
+    float sum = 0.f, acc[kDims];
+#pragma unroll
+    for (int c = 0; c < kDims; ++c) acc[c] = 0.f;
+    for (int first = (k0 / kChunk + warp) * kChunk; first < k1; first += W * kChunk) {
+      const int last = min(first + kChunk, k1);
+      for (int key = first; key < last; ++key) {
+        const int pi = key / a.c.page_size;
+        const int64_t page = table[pi];
+        if (page < 0 || page >= a.c.n_pages) continue;
+        const int64_t row = page * a.c.page_stride + (key - pi * a.c.page_size) * a.c.slot_stride;
+        float z = 0.f;
+        for (int d = lane; d < hd; d += 32) z = fmaf(to_f(qp[h * a.q.hs + d]), to_f(kp[row + d]), z);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) z += __shfl_xor_sync(0xffffffffu, z, x);
+        const float w = exp_above(z * a.scale, base);
+        sum += w;
+#pragma unroll
+        for (int c = 0; c < kDims; ++c)
+          if (c * 32 + lane < hd) acc[c] = fmaf(w, to_f(vp[row + c * 32 + lane]), acc[c]);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < kDims; ++c)
+      if (c * 32 + lane < hd) out[h * E::HDP + c * 32 + lane] = acc[c];
+    if (lane == 0) sm[h] = base, sl[h] = sum;
+    __syncwarp();
+  }
+}
+
+// As a call where the engine has registers to spare for one; within the kernel for the SIMT engines (one
+// head a group, 64 dims, runs: 42.2 us without it, 44.3 with a call, 42.6 within).
+template <typename E, int W>
+__device__ __noinline__ void redo_apart(const DecodeArgs& a, int64_t seq, int g, int j0, int heads, int k0,
+                                        int k1, float* out, float* sm, float* sl) {
+  redo_values<E, W>(a, seq, g, j0, heads, k0, k1, out, sm, sl);
+}
+
+// Keys k0 .. k1-1 of (sequence, KV head g), heads j0 .. j0+heads-1: this warp's share of them.
+// On return the accumulators are in the warp's ring, its maxima and sums in sm / sl; true where an
+// accumulator lies beyond kFarthest.
+template <typename E, int W>
+__device__ __forceinline__ bool warp_pass(const DecodeArgs& a, E& e, int64_t seq, int g, int j0,
                                           int heads, int k0, int k1, char* ring, char* wsh,
                                           char* bsh, float* sm, float* sl, int warp, int lane) {
   using T = typename E::T;
@@ -782,7 +859,10 @@ __device__ __forceinline__ void warp_pass(const DecodeArgs& a, E& e, int64_t seq
       sl[E::head(i, t)] = seen && l[i] == 0.f ? -1.f : l[i];
     }
   }
+  const bool far = __any_sync(0xffffffffu, beyond(e.acc));
   e.store(reinterpret_cast<float*>(ring), lane);
+  __syncwarp();
+  return far;
 }
 
 // Weight of a part with maximum pm and sum pl where the joined maximum is m.
@@ -859,8 +939,11 @@ __device__ __forceinline__ void block_piece(const DecodeArgs& a, E& e, int64_t s
   const int hd = a.c.hd;
   const int busy = min(W, (k1 - k0 + kChunk - 1) / kChunk);     // warps that get keys
   if (warp < busy) {
-    warp_pass<E, W>(a, e, seq, g, j0, heads, k0, k1, ring, wsh, bsh, sm + warp * E::kHeads,
-                    sl + warp * E::kHeads, warp, lane);
+    float *m = sm + warp * E::kHeads, *l = sl + warp * E::kHeads, *out = reinterpret_cast<float*>(ring);
+    if (warp_pass<E, W>(a, e, seq, g, j0, heads, k0, k1, ring, wsh, bsh, m, l, warp, lane)) {
+      if constexpr (E::kRedoApart) redo_apart<E, W>(a, seq, g, j0, heads, k0, k1, out, m, l);
+      else redo_values<E, W>(a, seq, g, j0, heads, k0, k1, out, m, l);
+    }
   }
   __syncthreads();
   const int cols = hd / 4;
