@@ -636,7 +636,9 @@ const char* tp_last_error(void);
 const char* tp_status_string(int32_t status);
 
 /* Waits for the stream, then reports (and clears) the device error word: TP_ERR_TIMEOUT if a
- * bounded device wait ran out since the last check, TP_ERR_CUDA on a CUDA error, else TP_OK. */
+ * bounded device wait ran out since the last check, TP_ERR_INDEX if an index in device memory was
+ * out of range (the paged cache), TP_ERR_CUDA on a CUDA error, else TP_OK.  Where both happened the
+ * wait is reported first and the index by the next check. */
 tp_status tp_check_device_error(void* stream);
 
 /* 1 if this build contains the sm_100a tensor-core kernels and the current device runs them. */

@@ -158,6 +158,8 @@ __global__ void wait_selftest_kernel(uint64_t limit_ns, uint32_t* err) {
   }
   __syncthreads();
 }
+
+__global__ void clear_bits_kernel(uint32_t* word, uint32_t bits) { atomicAnd(word, ~bits); }
 }  // namespace tp
 
 extern "C" {
@@ -245,16 +247,20 @@ tp_status tp_check_device_error(void* stream) {
   e = cudaMemcpy(&v, w, sizeof(v), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess)
     return tp::set_error(TP_ERR_CUDA, std::string("error word: ") + cudaGetErrorString(e));
-  if (v) {
-    const uint32_t zero = 0;
-    cudaMemcpy(w, &zero, sizeof(zero), cudaMemcpyHostToDevice);
-    if (v == tp::DEVERR_INDEX)
-      return tp::set_error(TP_ERR_INDEX,
-                           "a page, sequence or length in device memory was out of range");
-    return tp::set_error(TP_ERR_TIMEOUT,
-                         "a bounded device wait ran out (site bits " + std::to_string(v) + ")");
-  }
-  return TP_OK;
+  if (!v) return TP_OK;
+  // waits first; only the reported bits are cleared, so that the next check reports the others,
+  // those that kernels on other streams set meanwhile among them
+  const uint32_t waits = v & ~tp::DEVERR_INDEX, reported = waits ? waits : v;
+  tp::clear_bits_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(w, reported);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess)
+    return tp::set_error(TP_ERR_CUDA, std::string("error word: ") + cudaGetErrorString(e));
+  if (!waits)
+    return tp::set_error(TP_ERR_INDEX,
+                         "a page, sequence or length in device memory was out of range");
+  return tp::set_error(TP_ERR_TIMEOUT,
+                       "a bounded device wait ran out (site bits " + std::to_string(waits) + ")");
 }
 
 int32_t tp_tensor_core_path_available(void) { return tp::tensor_cores_usable() ? 1 : 0; }
