@@ -312,7 +312,9 @@ tp_status tp_rope(const tp_rope_desc* desc, int32_t dtype, int64_t T, int32_t n_
  * and tp_check_device_error() reports TP_ERR_INDEX.
  * k_pages, v_pages: 16-byte aligned, strides multiples of 16 bytes; head_dim a multiple of 8 in
  * [8, 256]; dtype bf16 or fp32; b <= 65535 (the library's other decode calls' limit); n_q <= 65535;
- * max_pages*page_size <= 2^30.
+ * max_pages*page_size <= 2^30.  Where scores are taken or kept, the arrays of all slots must fit an
+ * address: b * n_kv * max_pages*page_size * 4 bytes (with score: times the group's heads, rounded up to
+ * four) at most 2^56.
  * The workspaces hold nothing between calls; calls that may run at the same time need one each, and
  * their sizes are the current device's. */
 typedef struct {

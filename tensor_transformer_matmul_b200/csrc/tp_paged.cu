@@ -69,6 +69,15 @@ DecodePlan decode_plan(const tp::paged::View& c, int dtype) {
 // columns of a key's kept scores: the group's heads, in 16-byte vectors
 int score_columns(const tp::paged::View& c) { return static_cast<int>(tp::round_up(c.group, 4)); }
 
+// Arrays of the room of every table row: of ``columns`` floats a slot and KV head.  More bytes than
+// an address has are refused, before a size wraps around.
+tp_status check_room(const tp::paged::View& c, int columns) {
+  const double bytes = 4.0 * static_cast<double>(c.b) * c.n_kv * static_cast<double>(c.cap) * columns;
+  if (bytes > static_cast<double>(int64_t(1) << 56))
+    return set_error(TP_ERR_SHAPE, "b * n_kv * max_pages * page_size scores are too many");
+  return TP_OK;
+}
+
 struct DecodeWs {
   size_t lse, first, pm, pl, po, z, total;
 };
@@ -263,7 +272,9 @@ extern "C" tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, co
 extern "C" size_t tp_attn_decode_paged_workspace(const tp_paged_desc* desc, int32_t with_score) {
   tp::clear_error();
   tp::paged::View c;
-  return tp::paged::check_desc(desc, &c) == TP_OK ? decode_ws(c, desc->dtype, with_score != 0).total : 0;
+  if (tp::paged::check_desc(desc, &c) != TP_OK) return 0;
+  if (with_score && check_room(c, score_columns(c)) != TP_OK) return 0;
+  return decode_ws(c, desc->dtype, with_score != 0).total;
 }
 
 extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_head_rows* q,
@@ -275,6 +286,7 @@ extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_he
   tp::paged::DecodeArgs a{};
   tp_status st = tp::paged::check_desc(desc, &a.c);
   if (st != TP_OK) return st;
+  if (score && (st = check_room(a.c, score_columns(a.c))) != TP_OK) return st;
   if (desc->b == 0) return TP_OK;
   const int eb = tp::elem_bytes(desc->dtype);
   if ((st = tp::paged::check_pages(k_pages, v_pages, tables)) != TP_OK ||
@@ -335,7 +347,7 @@ extern "C" tp_status tp_attn_decode_paged(const tp_paged_desc* desc, const tp_he
 extern "C" size_t tp_kv_evict_paged_workspace(const tp_paged_desc* desc, int32_t budget) {
   tp::clear_error();
   tp::paged::View c;
-  if (tp::paged::check_desc(desc, &c) != TP_OK) return 0;
+  if (tp::paged::check_desc(desc, &c) != TP_OK || check_room(c, 1) != TP_OK) return 0;
   return budget >= 1 && budget <= c.cap ? evict_ws(c, budget) : 0;
 }
 
@@ -347,7 +359,7 @@ extern "C" tp_status tp_kv_evict_paged(const tp_paged_desc* desc, void* score, c
   tp::clear_error();
   tp::paged::EvictArgs a{};
   tp_status st = tp::paged::check_desc(desc, &a.c);
-  if (st != TP_OK) return st;
+  if (st != TP_OK || (st = check_room(a.c, 1)) != TP_OK) return st;
   if (budget < 1 || budget > a.c.cap)
     return set_error(TP_ERR_SHAPE, "budget must be in [1, max_pages * page_size]");
   if (recent < 0 || recent > budget) return set_error(TP_ERR_SHAPE, "recent must be in [0, budget]");
