@@ -1,4 +1,6 @@
 // Rotary positions and the paged key/value cache: argument checks and launches.
+#include <atomic>
+
 #include "paged.cuh"
 #include "paged_decode.cuh"
 
@@ -97,14 +99,16 @@ DecodeWs decode_ws(const tp::paged::View& c, int dtype, bool with_score) {
   return w;
 }
 
-// Lets a kernel use ``bytes`` of dynamic shared memory; done: per device, whether it may already.
+// Lets a kernel use ``bytes`` of dynamic shared memory; done: per device, whether it may already
+// (host threads may meet here: setting the limit twice is the same as once).
+using Done = std::atomic<bool>[64];
 template <typename K>
-tp_status allow_smem(K* kern, int bytes, int (&done)[64]) {
+tp_status allow_smem(K* kern, int bytes, Done& done) {
   int dev = 0;
   TP_CUDA_TRY(cudaGetDevice(&dev));
-  if (dev < 64 && done[dev]) return TP_OK;
+  if (dev < 64 && done[dev].load(std::memory_order_acquire)) return TP_OK;
   TP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
-  if (dev < 64) done[dev] = 1;
+  if (dev < 64) done[dev].store(true, std::memory_order_release);
   return TP_OK;
 }
 
@@ -112,7 +116,7 @@ template <typename E, int W>
 tp_status launch_whole(const tp::paged::DecodeArgs& a, dim3 grid, cudaStream_t s) {
   constexpr int smem = tp::paged::decode_smem<E>(W);
   auto* whole = tp::paged::decode_whole_kernel<E, W>;
-  static int done[64];
+  static Done done;
   const tp_status st = allow_smem(whole, smem, done);
   if (st != TP_OK) return st;
   TP_LAUNCH_PDL(whole, grid, dim3(W * 32), smem, s, a);
@@ -135,7 +139,7 @@ tp_status launch_decode(const tp::paged::DecodeArgs& a, const DecodePlan& p, cud
   }
   constexpr int smem = decode_smem<E>(kSplit);
   auto* split = decode_split_kernel<E>;
-  static int done[64];
+  static Done done;
   const tp_status st = allow_smem(split, smem, done);
   if (st != TP_OK) return st;
   TP_LAUNCH_PDL(split, dim3(static_cast<unsigned>(a.runs)), dim3(kSplit * 32), smem, s, a);
@@ -398,7 +402,7 @@ extern "C" tp_status tp_kv_evict_paged(const tp_paged_desc* desc, void* score, c
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   {
     tp::ProfScope prof(s, "kv_evict_select");
-    static int done[64];
+    static Done done;
     if ((st = allow_smem(tp::paged::evict_select_kernel, tp::paged::kEvictRoom * 4, done)) != TP_OK) return st;
     const int smem = a.room * 4;
     TP_LAUNCH_PDL(tp::paged::evict_select_kernel,
@@ -409,7 +413,7 @@ extern "C" tp_status tp_kv_evict_paged(const tp_paged_desc* desc, void* score, c
   const dim3 grid(static_cast<unsigned>(2 * a.strips), static_cast<unsigned>(desc->n_kv),
                   static_cast<unsigned>(desc->b));
   constexpr int smem = tp::paged::kMoveWarps * tp::paged::kMoveRing;
-  static int done[64];
+  static Done done;
   if ((st = allow_smem(tp::paged::evict_move_kernel, smem, done)) != TP_OK) return st;
   TP_LAUNCH_PDL(tp::paged::evict_move_kernel, grid, dim3(tp::paged::kMoveWarps * 32), smem, s, a, eb);
   return TP_OK;
