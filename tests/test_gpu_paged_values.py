@@ -18,9 +18,9 @@ from tests.test_gpu_paged import HALF_STEP, U, Cache
 
 pytestmark = pytest.mark.gpu
 INF = float("inf")
-# near the largest number: above bf16's largest (3.3895e38) for fp32, below it for bf16, so that a mean
-# of equal values does not round to infinity
-HUGE = {"f32": 3.395e38, "bf16": 3.35e38}
+# near the largest number (3.4028e38), and for fp32 above 3.3962e38, where numbers round to an infinite
+# bf16; below bf16's largest (3.3895e38) for bf16.  A mean of equal ones does not round to infinity.
+HUGE = {"f32": 3.398e38, "bf16": 3.35e38}
 
 GROUPS = [(1, "bf16"), (4, "bf16"), (8, "bf16"), (16, "bf16"), (1, "f32"), (4, "f32"), (8, "f32"),
           (16, "f32")]
