@@ -254,7 +254,8 @@ tp_status tp_attn_unpack_grads(const tp_attn_desc* desc, const void* dwqkv_p, co
  *                     g = clamp((r_i - beta_slow)/(beta_fast - beta_slow), 0, 1):
  *                     g w_i + (1 - g) w_i / factor; magnitude 1 + 0.1 ln(factor) unless given
  * Angles are computed in 64 bits and reduced to one turn before the sine and cosine, so far
- * positions lose nothing; the rotation is computed in fp32 and rounded once. */
+ * positions lose nothing; sine, cosine and the rotation are computed in fp32 (within 5e-7 of
+ * m (|x1| + |x2|)) and the result is rounded once. */
 typedef enum { TP_ROPE_HALF = 0, TP_ROPE_INTERLEAVED = 1 } tp_rope_layout;
 typedef enum {
   TP_ROPE_PLAIN = 0, TP_ROPE_LINEAR = 1, TP_ROPE_NTK = 2, TP_ROPE_BY_PARTS = 3
@@ -275,7 +276,8 @@ typedef struct {
 
 /* Rows of heads: row (t, j) is head_dim consecutive elements at data + t*token_stride +
  * j*head_stride (strides in elements, >= 0).  Describes [T][heads][head_dim] tensors, slices of
- * them, and [heads][T][head_dim] ones.  Rows that a call writes must not overlap each other. */
+ * them, and [heads][T][head_dim] ones.  Rows that a call writes must not overlap each other: the
+ * smaller stride at least head_dim, the larger one past all rows of the smaller. */
 typedef struct {
   const void* data;
   int64_t token_stride;
@@ -357,7 +359,8 @@ tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, const void* s
  *   as they are.
  * Scores, softmax statistics, weights and sums are fp32 (bf16 products are exact, the weights enter
  * the second product with 16 bits, fp32 products are taken from numbers cut into three bf16 parts
- * where a group has more than four heads); o is rounded once.  A key whose score is -infinity has
+ * where a group has more than four heads, which takes places from numbers below 2^-109; exponentials
+ * are 2^x within 2^-22); o is rounded once.  A key whose score is -infinity has
  * weight 0; if all scores are, o is NaN, and so it is where a score is NaN or +infinity.  Values enter
  * as in IEEE arithmetic: an infinite one gives the infinity of its sign where its weight is not 0 (of
  * both signs, or of weight 0: NaN), finite ones a finite mean however large they are.

@@ -125,3 +125,36 @@ def test_pages_outside_the_pool_with_infinite_values(lib):
     with pytest.raises(lib.TpError) as e:
         lib.tp_check_device_error()
     assert e.value.status == lib.TP_ERR_INDEX
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("group", [1, 8])
+def test_many_rows_in_runs(lib, group, dtype):
+    # more rows than runs, so that a run ends one row and begins others: infinities and the largest
+    # values in rows of every position of a run, and the weights of rows that were taken again
+    lens = [(37 * i) % 101 + 1 for i in range(100)] + [2500, 33]
+    c = cache(lib, group, dtype, 64, 2000, lens=lens)
+    for i in range(0, len(lens), 3):
+        put(c, c.vp, i, i & 1, lens[i] // 2, i % 64, INF if i % 2 else -INF)
+        put(c, c.vp, i, 1 - (i & 1), lens[i] - 1, 63 - i % 64, HUGE[dtype])
+    before = f64(c.score)
+    o, lse = c.decode()
+    check(c, o, lse)
+    kp, _, tables = c.host()
+    q, got = f64(c.q), f64(c.score)
+    for i, n in enumerate(lens):
+        _, pg, at = opaged.slots_of(tables, i, n, c.page, kp.shape[0])
+        for g in range(c.n_kv):
+            hs = slice(g * group, (g + 1) * group)
+            k = kp[pg, g, at]
+            z = c.hd ** -0.5 * q[i, hs] @ k.T
+            w = np.exp(z - z.max(1, keepdims=True))
+            w /= w.sum(1, keepdims=True)
+            dz = (c.hd ** -0.5 * (np.abs(q[i, hs]) @ np.abs(k).T) * (2 * c.hd + 4) * U
+                  + 4 * U * np.abs(z)).max(1, keepdims=True)
+            # (its score, and the log-sum's error of check())
+            want = before[i, g, :n] + w.sum(0)
+            tol = (w * (2 * dz + (2 * n + 96) * U)).sum(0) + U * np.abs(want)
+            assert (np.abs(got[i, g, :n] - want) <= tol).all(), (i, g)
+            assert np.array_equal(got[i, g, n:], before[i, g, n:])
+    lib.tp_check_device_error()
