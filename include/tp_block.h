@@ -363,7 +363,8 @@ tp_status tp_kv_append_paged(const tp_paged_desc* desc, int64_t T, const void* s
  * are 2^x within 2^-22); o is rounded once.  A key whose score is -infinity has
  * weight 0; if all scores are, o is NaN, and so it is where a score is NaN or +infinity.  Values enter
  * as in IEEE arithmetic: an infinite one gives the infinity of its sign where its weight is not 0 (of
- * both signs, or of weight 0: NaN), finite ones a finite mean however large they are.
+ * both signs, or of weight 0: NaN), finite ones a finite mean however large they are (where sums exceed
+ * 2^114 keys are taken twice, more slowly).
  * The sum over the keys is split over the SMs and joined in a fixed order: equal calls on equal
  * devices give equal results.  Slots at and past lens[i] are not read.
  * workspace: tp_attn_decode_paged_workspace(desc, score != NULL) bytes, 16-byte aligned.  It grows
