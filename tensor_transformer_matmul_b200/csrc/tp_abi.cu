@@ -251,9 +251,10 @@ tp_status tp_check_device_error(void* stream) {
   // waits first; only the reported bits are cleared, so that the next check reports the others,
   // those that kernels on other streams set meanwhile among them
   const uint32_t waits = v & ~tp::DEVERR_INDEX, reported = waits ? waits : v;
-  tp::clear_bits_kernel<<<1, 1, 0, static_cast<cudaStream_t>(stream)>>>(w, reported);
+  // (on the current device's default stream, as the copy above: the word is that device's)
+  tp::clear_bits_kernel<<<1, 1>>>(w, reported);
   e = cudaGetLastError();
-  if (e == cudaSuccess) e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
   if (e != cudaSuccess)
     return tp::set_error(TP_ERR_CUDA, std::string("error word: ") + cudaGetErrorString(e));
   if (!waits)
